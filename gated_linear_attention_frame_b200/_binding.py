@@ -31,6 +31,7 @@ EXPORTED = ("gla_forward", "gla_forward_timed", "gla_forward_noalloc", "gla_noal
             "gla_softmax_anchor", "gla_softmax_anchor_timed", "gla_softmax_anchor_step",
             "gla_backward", "gla_backward_timed", "gla_saved_bytes", "gla_forward_train",
             "gla_backward_saved", "gla_backward_saved_timed",
+            "gla_cache_plan", "gla_cache_store", "gla_cache_attention",
             "gla_trim_workspace", "gla_set_workspace_retention", "gla_inject_alloc_failure",
             "gla_set_wait_limit_ns", "gla_inject_stall", "gla_error_string", "gla_device_fault",
             "gla_version")
@@ -109,6 +110,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.gla_backward_saved.restype = i32
     lib.gla_backward_saved_timed.argtypes = bwds + [ctypes.POINTER(vp)]
     lib.gla_backward_saved_timed.restype = i32
+    lib.gla_cache_plan.argtypes = [vp] * 12 + [i32] * 8 + [vp]
+    lib.gla_cache_plan.restype = i32
+    lib.gla_cache_store.argtypes = [vp] * 10 + [i32] * 6 + [vp]
+    lib.gla_cache_store.restype = i32
+    lib.gla_cache_attention.argtypes = [vp] * 10 + [i32] * 12 + [f32, vp]
+    lib.gla_cache_attention.restype = i32
     lib.gla_noalloc_scratch_bytes.argtypes = []
     lib.gla_noalloc_scratch_bytes.restype = ctypes.c_size_t
     lib.gla_trim_workspace.argtypes = []

@@ -1,0 +1,235 @@
+"""ctypes binding of the paged 8-bit rollout cache (gla_cache_plan,
+gla_cache_store, gla_cache_attention; include/gla.h) and a small container for
+its tensors.
+
+As in _binding, only argument marshalling happens here.  Beside the library's
+own checks the wrappers compare dtypes and element counts with the sizes that
+are passed, and run on the device of the tensors, whichever device is current.
+
+    cache = gla.rollout_cache(sequences=8, pages=4096, kv_heads=24, d=128,
+                              max_pages=512, page_tokens=64, frame_tokens=3680,
+                              window_frames=4, n_sink=256)
+    plan = gla.cache_plan(cache, new_lens, tokens)      # once a step
+    gla.cache_store(cache, plan, k, v)                  # each layer (its own pools)
+    out = gla.cache_attention(cache, plan, q)
+"""
+
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import _binding as _b
+
+_I32, _F32, _BF16, _FP8, _U8 = (torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn,
+                                torch.uint8)
+
+
+class _Call:
+    """Checks of one call's tensors: kind, layout, size and one common device."""
+
+    __slots__ = ("where", "device")
+
+    def __init__(self, where: str):
+        self.where = where
+        self.device = None
+
+    def __call__(self, name, x, dtypes, count):
+        """Device pointer of `x` (None -> NULL), which must hold at least
+        `count` elements of one of `dtypes`."""
+        if x is None:
+            return None
+        if isinstance(x, int):
+            return x
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("%s: %s must be a torch.Tensor, an int address or None, got %r"
+                            % (self.where, name, type(x)))
+        if x.dtype not in dtypes:
+            raise TypeError("%s: %s must be %s, got %s"
+                            % (self.where, name, " or ".join(str(d) for d in dtypes), x.dtype))
+        if not x.is_cuda:
+            raise ValueError("%s: %s must be on a CUDA device (got %s)"
+                             % (self.where, name, x.device))
+        if not x.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (self.where, name))
+        if x.numel() < count:
+            raise ValueError("%s: %s holds %d elements, the sizes ask for %d"
+                             % (self.where, name, x.numel(), count))
+        i = x.get_device()
+        if self.device is None:
+            self.device = i
+        elif self.device != i:
+            raise ValueError("%s: %s is on cuda:%d, other tensors are on cuda:%d"
+                             % (self.where, name, i, self.device))
+        return x.data_ptr() or None
+
+    def run(self, fn, args, stream):
+        """fn(*args, stream) on the tensors' device; a nonzero status raises."""
+        if self.device is None or self.device == torch.cuda.current_device():
+            st = fn(*args, _b._stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(*args, _b._stream(stream))
+        if st != _b.GLA_OK:
+            raise _b.GLAError(st, self.where)
+
+
+def gla_cache_plan(lens, held, new_lens, free_count, free_pages, block_table, lens_out, held_out,
+                   free_count_out, cu_tokens, slots, status, R, max_pages, pages, page_tokens,
+                   tokens, frame_tokens, window_frames, n_sink, stream=None) -> None:
+    """Lengths, pages and slots of one step (see include/gla.h).  All arrays
+    int32; raises GLAError on a nonzero return code.  Whether the step was
+    admitted is in status[0] on the GPU."""
+    c = _Call("gla_cache_plan")
+    i = (_I32,)
+    args = (c("lens", lens, i, R), c("held", held, i, R), c("new_lens", new_lens, i, R),
+            c("free_count", free_count, i, 1), c("free_pages", free_pages, i, pages),
+            c("block_table", block_table, i, R * max_pages), c("lens_out", lens_out, i, R),
+            c("held_out", held_out, i, R), c("free_count_out", free_count_out, i, 1),
+            c("cu_tokens", cu_tokens, i, R + 1), c("slots", slots, i, tokens),
+            c("status", status, i, 1), R, max_pages, pages, page_tokens, tokens, frame_tokens,
+            window_frames, n_sink)
+    c.run(_b.load_library().gla_cache_plan, args, stream)
+
+
+def gla_cache_store(k, v, lens, cu_tokens, slots, k_cache, v_cache, k_scale, v_scale, nonfinite,
+                    R, tokens, Hkv, d, pages, page_tokens, stream=None) -> None:
+    """Quantise the new tokens' keys and values into the cache (see
+    include/gla.h).  `nonfinite`: int32 counter tensor or None."""
+    c = _Call("gla_cache_store")
+    i, new, code = (_I32,), tokens * Hkv * d, pages * Hkv * page_tokens * d
+    args = (c("k", k, (_BF16,), new), c("v", v, (_BF16,), new), c("lens", lens, i, R),
+            c("cu_tokens", cu_tokens, i, R + 1), c("slots", slots, i, tokens),
+            c("k_cache", k_cache, (_FP8, _U8), code), c("v_cache", v_cache, (_FP8, _U8), code),
+            c("k_scale", k_scale, (_F32,), pages * Hkv),
+            c("v_scale", v_scale, (_F32,), pages * Hkv), c("nonfinite", nonfinite, i, 1), R,
+            tokens, Hkv, d, pages, page_tokens)
+    c.run(_b.load_library().gla_cache_store, args, stream)
+
+
+def gla_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_tokens,
+                        gate_z, out, R, tokens, max_new, H, Hkv, d, pages, page_tokens, max_pages,
+                        frame_tokens, window_frames, n_sink, scale, stream=None) -> None:
+    """Attention of the new tokens over the cache (see include/gla.h)."""
+    c = _Call("gla_cache_attention")
+    i, new, code = (_I32,), tokens * H * d, pages * Hkv * page_tokens * d
+    args = (c("q", q, (_BF16,), new), c("k_cache", k_cache, (_FP8, _U8), code),
+            c("v_cache", v_cache, (_FP8, _U8), code), c("k_scale", k_scale, (_F32,), pages * Hkv),
+            c("v_scale", v_scale, (_F32,), pages * Hkv),
+            c("block_table", block_table, i, R * max_pages), c("lens", lens, i, R),
+            c("cu_tokens", cu_tokens, i, R + 1), c("gate_z", gate_z, (_BF16,), new),
+            c("out", out, (_BF16,), new), R, tokens, max_new, H, Hkv, d, pages, page_tokens,
+            max_pages, frame_tokens, window_frames, n_sink, scale)
+    c.run(_b.load_library().gla_cache_attention, args, stream)
+
+
+@dataclass
+class RolloutCache:
+    """The tensors of a paged rollout cache and its mask.  k, v and their
+    scales belong to one layer: layers share the lengths and tables, so further
+    layers are `cache.layer()`s of the first."""
+
+    k: torch.Tensor            # float8_e4m3fn [pages, kv_heads, page_tokens, d]
+    v: torch.Tensor
+    k_scale: torch.Tensor      # fp32 [pages, kv_heads]
+    v_scale: torch.Tensor
+    lens: torch.Tensor         # int32 [sequences]: tokens held
+    held: torch.Tensor         # int32 [sequences]: first page behind the sinks still held
+    block_table: torch.Tensor  # int32 [sequences, max_pages]
+    free_pages: torch.Tensor   # int32 [pages]: stack of free pages
+    free_count: torch.Tensor   # int32 [1]
+    frame_tokens: int = 1
+    window_frames: int = 0
+    n_sink: int = 0
+
+    @property
+    def page_tokens(self) -> int:
+        return self.k.shape[2]
+
+    def layer(self) -> "RolloutCache":
+        """The cache of another layer: pools of its own, the same tables."""
+        return RolloutCache(torch.zeros_like(self.k), torch.zeros_like(self.v),
+                            torch.ones_like(self.k_scale), torch.ones_like(self.v_scale),
+                            self.lens, self.held, self.block_table, self.free_pages,
+                            self.free_count, self.frame_tokens, self.window_frames, self.n_sink)
+
+
+@dataclass
+class CachePlan:
+    """What one step adds: row ranges and slots of the new tokens."""
+
+    cu_tokens: torch.Tensor  # int32 [sequences + 1]
+    slots: torch.Tensor      # int32 [tokens]
+    status: torch.Tensor     # int32 [1]; 0: admitted (see gla_cache_plan)
+
+
+def rollout_cache(sequences: int, pages: int, kv_heads: int, d: int, max_pages: int,
+                  page_tokens: int = 64, frame_tokens: int = 1, window_frames: int = 0,
+                  n_sink: int = 0, device="cuda") -> RolloutCache:
+    """An empty cache: every page free, every sequence of length 0."""
+    if page_tokens not in (16, 32, 64, 128):
+        raise ValueError("page_tokens must be 16, 32, 64 or 128, got %d" % page_tokens)
+    if d not in (64, 128):
+        raise ValueError("d must be 64 or 128, got %d" % d)
+    shape = (pages, kv_heads, page_tokens, d)
+    codes = [torch.zeros(shape, dtype=_U8, device=device).view(_FP8) for _ in range(2)]
+    scales = [torch.ones(pages, kv_heads, dtype=_F32, device=device) for _ in range(2)]
+    ints = lambda *s: torch.zeros(*s, dtype=_I32, device=device)  # noqa: E731
+    # the stack's top is its last entry: pages come out in ascending order
+    free = torch.arange(pages - 1, -1, -1, dtype=_I32, device=device)
+    return RolloutCache(codes[0], codes[1], scales[0], scales[1], ints(sequences),
+                        ints(sequences), ints(sequences, max_pages) - 1, free, ints(1) + pages,
+                        frame_tokens, window_frames, n_sink)
+
+
+def cache_plan(cache: RolloutCache, new_lens, tokens: int, stream=None) -> CachePlan:
+    """Plan one step in place: `new_lens` int32 [sequences] on the GPU (negative:
+    the sequence has ended), `tokens` rows of the packed arrays (their sum, or
+    more).  Updates the cache's lengths, tables and free pages."""
+    R, max_pages = cache.block_table.shape
+    dev = cache.lens.device
+    plan = CachePlan(torch.empty(R + 1, dtype=_I32, device=dev),
+                     torch.empty(tokens, dtype=_I32, device=dev),
+                     torch.empty(1, dtype=_I32, device=dev))
+    gla_cache_plan(cache.lens, cache.held, new_lens, cache.free_count, cache.free_pages,
+                   cache.block_table, cache.lens, cache.held, cache.free_count, plan.cu_tokens,
+                   plan.slots, plan.status, R, max_pages, cache.k.shape[0], cache.page_tokens,
+                   tokens, cache.frame_tokens, cache.window_frames, cache.n_sink, stream)
+    return plan
+
+
+def cache_store(cache: RolloutCache, plan: CachePlan, k, v, nonfinite=None, stream=None) -> None:
+    """Quantise k, v [tokens, kv_heads, d] of the step into the cache."""
+    pages, H, P, d = cache.k.shape
+    if k.shape != (plan.slots.numel(), H, d) or v.shape != k.shape:
+        raise ValueError("k, v must be [%d, %d, %d], got %s and %s"
+                         % (plan.slots.numel(), H, d, tuple(k.shape), tuple(v.shape)))
+    gla_cache_store(k, v, cache.lens, plan.cu_tokens, plan.slots, cache.k, cache.v, cache.k_scale,
+                    cache.v_scale, nonfinite, cache.lens.numel(), k.shape[0], H, d, pages, P,
+                    stream)
+
+
+def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=None, out=None,
+                    max_new=None, stream=None):
+    """Attention of the step's queries q [tokens, H, d] over the cache (which
+    already holds the step's keys and values); returns out.  `max_new`: the
+    most new tokens of one sequence, if the host knows it (default: tokens)."""
+    pages, Hkv, P, d = cache.k.shape
+    R, max_pages = cache.block_table.shape
+    N, H = q.shape[0], q.shape[1]
+    if q.shape != (plan.slots.numel(), H, d):
+        raise ValueError("q must be [%d, H, %d], got %s" % (plan.slots.numel(), d, tuple(q.shape)))
+    if gate_z is not None and gate_z.shape != q.shape:
+        raise ValueError("gate_z must have q's shape, got %s" % (tuple(gate_z.shape),))
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape, got %s" % (tuple(out.shape),))
+    gla_cache_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.block_table,
+                        cache.lens, plan.cu_tokens, gate_z, out, R, N,
+                        N if max_new is None else max_new, H, Hkv, d, pages, P, max_pages,
+                        cache.frame_tokens, cache.window_frames, cache.n_sink,
+                        1.0 / math.sqrt(d) if scale is None else scale, stream)
+    return out

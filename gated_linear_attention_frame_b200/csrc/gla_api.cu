@@ -37,6 +37,8 @@
 #include "gla.h"
 #include "gla_bwd_kv.cuh"
 #include "gla_bwd_q.cuh"
+#include "gla_cache.cuh"
+#include "gla_cache_token.cuh"
 #include "gla_common.cuh"
 #include "gla_gdn_scan.cuh"
 #include "gla_increment.cuh"
@@ -186,6 +188,21 @@ cudaError_t set_smem_attrs() {
                               gla::ScanBwdCfg<128>::kSmemBytes);
 }
 
+cudaError_t set_cache_attrs() {
+  cudaError_t e = cudaFuncSetAttribute(gla::gla_cache_plan_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (4 * gla::kCacheMaxSeqs + 3) * 4);
+  if (e != cudaSuccess) return e;
+  constexpr int kPre = (gla::kCacheMaxSeqs + 1) * 8;
+  e = cudaFuncSetAttribute(gla::gla_cache_token_kernel<64>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gla::TokenCfg<64>::kFixedBytes + kPre);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gla::gla_cache_token_kernel<128>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              gla::TokenCfg<128>::kFixedBytes + kPre);
+}
+
 // Per-device one-time set-up: SM count, architecture check, kernel attributes,
 // the driver's tensor-map encoder.
 int device_setup(DeviceInfo* out) {
@@ -199,7 +216,7 @@ int device_setup(DeviceInfo* out) {
     if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return GLA_ERR_DEVICE;
     if (prop.major != 10) return GLA_ERR_DEVICE;
     if (set_smem_attrs<32>() != cudaSuccess || set_smem_attrs<64>() != cudaSuccess ||
-        set_smem_attrs<128>() != cudaSuccess)
+        set_smem_attrs<128>() != cudaSuccess || set_cache_attrs() != cudaSuccess)
       return GLA_ERR_LAUNCH;
     if (g_encode == nullptr) {
       void* fn = nullptr;
@@ -939,6 +956,175 @@ int anchor_impl(const void* q, const void* k, const void* v, const void* z, void
   return status;
 }
 
+// ------------------------------------------------ paged 8-bit rollout cache
+
+bool cache_page_ok(int P) { return P == 16 || P == 32 || P == 64 || P == 128; }
+
+// Sizes every call on the cache shares; host only.
+int validate_cache(int R, int tokens, int pages, int P) {
+  if (R < 0 || tokens < 0 || pages < 0) return GLA_ERR_SHAPE;
+  if (!cache_page_ok(P) || R > gla::kCacheMaxSeqs) return GLA_ERR_SHAPE;
+  if (static_cast<int64_t>(pages) * P > INT32_MAX) return GLA_ERR_SHAPE;  // slots are 32-bit
+  if (tokens > (1 << 30)) return GLA_ERR_SHAPE;
+  return GLA_OK;
+}
+
+// Window and sinks of a call on the cache; host only.
+int validate_cache_window(int F, int W, int n_sink) {
+  return (F < 1 || W < 0 || n_sink < 0) ? GLA_ERR_SHAPE : GLA_OK;
+}
+
+int cache_plan_impl(const gla::PlanParams& p, cudaStream_t stream) {
+  int st = validate_cache(p.R, p.tokens, p.pages, p.P);
+  if (st != GLA_OK) return st;
+  if ((st = validate_cache_window(p.F, p.W, p.n_sink)) != GLA_OK) return st;
+  if (p.max_pages < 0 || static_cast<int64_t>(p.max_pages) * p.P > INT32_MAX) return GLA_ERR_SHAPE;
+  if (p.free_count == nullptr || p.free_count_out == nullptr || p.cu == nullptr ||
+      p.status == nullptr)
+    return GLA_ERR_NULL;
+  if (p.R > 0 && (p.lens == nullptr || p.held == nullptr || p.new_lens == nullptr ||
+                  p.lens_out == nullptr || p.held_out == nullptr))
+    return GLA_ERR_NULL;
+  if ((p.R > 0 && p.max_pages > 0 && p.table == nullptr) ||
+      (p.pages > 0 && p.free_pages == nullptr) || (p.tokens > 0 && p.slots == nullptr))
+    return GLA_ERR_NULL;
+  const void* all[] = {p.lens,  p.held,     p.new_lens, p.free_count,     p.free_pages, p.table,
+                       p.lens_out, p.held_out, p.free_count_out, p.cu, p.slots, p.status};
+  for (const void* x : all)
+    if (!aligned(x, 4)) return GLA_ERR_ALIGN;
+  DeviceInfo di;
+  if ((st = device_setup(&di)) != GLA_OK) return st;
+  // one CTA up to 8192 tokens and 1024 sequences (its launch is the shorter
+  // one), the largest portable cluster above
+  const int ctas = p.tokens > 8192 || p.R > gla::kPlanThreads ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(gla::kPlanThreads);
+  cfg.dynamicSmemBytes = (4 * static_cast<size_t>(p.R) + 3) * sizeof(int);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_plan_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return GLA_ERR_LAUNCH;
+  }
+  return GLA_OK;
+}
+
+using StoreKernel = void (*)(const gla::StoreParams);
+template <int D>
+StoreKernel store_kernel(int P) {
+  switch (P) {
+    case 16: return gla::gla_cache_store_kernel<D, 16>;
+    case 32: return gla::gla_cache_store_kernel<D, 32>;
+    case 64: return gla::gla_cache_store_kernel<D, 64>;
+    default: return gla::gla_cache_store_kernel<D, 128>;
+  }
+}
+
+int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t stream) {
+  if (d != 64 && d != 128) return GLA_ERR_UNSUPPORTED_D;
+  int st = validate_cache(p.R, p.tokens, p.pages, P);
+  if (st != GLA_OK) return st;
+  if (p.H < 0 || p.H > (1 << 16)) return GLA_ERR_SHAPE;
+  if (p.R == 0 || p.tokens == 0 || p.H == 0 || p.pages == 0) return GLA_OK;
+  if (p.k == nullptr || p.v == nullptr || p.lens == nullptr || p.cu == nullptr ||
+      p.slots == nullptr || p.k8 == nullptr || p.v8 == nullptr || p.ks == nullptr ||
+      p.vs == nullptr)
+    return GLA_ERR_NULL;
+  if (!aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.k8, 16) || !aligned(p.v8, 16))
+    return GLA_ERR_ALIGN;
+  const void* small[] = {p.lens, p.cu, p.slots, p.ks, p.vs, p.nonfinite};
+  for (const void* x : small)
+    if (!aligned(x, 4)) return GLA_ERR_ALIGN;
+  DeviceInfo di;
+  if ((st = device_setup(&di)) != GLA_OK) return st;
+  // at most one item for each page the tokens can touch, head and tensor
+  const int64_t runs = static_cast<int64_t>(p.tokens) / P + 2 * static_cast<int64_t>(p.R);
+  const int64_t items = (runs < p.tokens ? runs : p.tokens) * p.H * 2;
+  const int64_t most = static_cast<int64_t>(di.sms) * 16;
+  const int grid = static_cast<int>(items < most ? items : most);
+  const size_t smem = (static_cast<size_t>(p.R) + 1) * sizeof(int);
+  StoreKernel fn = d == 64 ? store_kernel<64>(P) : store_kernel<128>(P);
+  fn<<<grid, gla::kStoreThreads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+}
+
+template <int D>
+int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t stream) {
+  using C = gla::TokenCfg<D>;
+  const int grid = di.sms * C::kCtasPerSm;
+  const int64_t desc_bytes = align256(static_cast<int64_t>(grid) * 32);
+  const int64_t part_bytes = static_cast<int64_t>(grid) * 2 * C::kPartFloats * 4;
+  uint8_t* ws = nullptr;
+  int status = take_workspace(desc_bytes + part_bytes, stream, &ws);
+  if (status != GLA_OK) return status;
+  p.desc = reinterpret_cast<int*>(ws);
+  p.part = reinterpret_cast<float*>(ws + desc_bytes);
+  const size_t smem = C::kFixedBytes + (static_cast<size_t>(p.R) + 1) * 8;
+  gla::gla_cache_token_kernel<D><<<grid, C::kThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) status = GLA_ERR_LAUNCH;
+  if (status == GLA_OK) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, C::kRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p, int(C::kPartFloats),
+                           int(C::kRows)) != cudaSuccess) {
+      cudaGetLastError();
+      status = GLA_ERR_LAUNCH;
+    }
+  }
+  if (cudaFreeAsync(ws, stream) != cudaSuccess) {
+    cudaGetLastError();
+    if (status == GLA_OK) status = GLA_ERR_LAUNCH;
+  }
+  return status;
+}
+
+int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, float scale,
+                         cudaStream_t stream) {
+  if (d != 64 && d != 128) return GLA_ERR_UNSUPPORTED_D;
+  int st = validate_cache(p.R, p.tokens, p.pages, P);
+  if (st != GLA_OK) return st;
+  if ((st = validate_cache_window(p.F, p.W, p.n_sink)) != GLA_OK) return st;
+  if (max_new < 0 || p.H < 0 || p.Hkv < 0 || p.H > (1 << 16)) return GLA_ERR_SHAPE;
+  if (p.max_pages < 0 || static_cast<int64_t>(p.max_pages) * P > INT32_MAX - 256)
+    return GLA_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return GLA_ERR_SHAPE;  // rejects NaN and inf
+  if (p.R == 0 || p.tokens == 0 || p.H == 0) return GLA_OK;
+  if (p.Hkv == 0 || p.H % p.Hkv != 0 || p.H / p.Hkv > 128) return GLA_ERR_SHAPE;
+  if (p.q == nullptr || p.out == nullptr || p.lens == nullptr || p.cu == nullptr)
+    return GLA_ERR_NULL;
+  if (p.pages > 0 && p.max_pages > 0 &&
+      (p.k8 == nullptr || p.v8 == nullptr || p.ks == nullptr || p.vs == nullptr ||
+       p.table == nullptr))
+    return GLA_ERR_NULL;
+  if (!aligned(p.q, 16) || !aligned(p.out, 16) || !aligned(p.k8, 16) || !aligned(p.v8, 16) ||
+      !aligned(p.z, 16))
+    return GLA_ERR_ALIGN;
+  const void* small[] = {p.ks, p.vs, p.table, p.lens, p.cu};
+  for (const void* x : small)
+    if (!aligned(x, 4)) return GLA_ERR_ALIGN;
+  p.G = p.H / p.Hkv;
+  p.p_shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
+  p.sl2 = static_cast<float>(1.4426950408889634 * scale);
+  if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
+  DeviceInfo di;
+  if ((st = device_setup(&di)) != GLA_OK) return st;
+  return d == 64 ? run_cache_token<64>(p, di, stream) : run_cache_token<128>(p, di, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1114,6 +1300,68 @@ int gla_backward_saved_timed(const void* q, const void* k, const void* v,
             dgate_logits, dstate_in, B, H, frames, tokens_per_frame, d, eps, stream,
             static_cast<const uint8_t*>(saved)};
   return backward_saved(a, events);
+}
+
+int gla_cache_plan(const int* lens, const int* held, const int* new_lens, const int* free_count,
+                   int* free_pages, int* block_table, int* lens_out, int* held_out,
+                   int* free_count_out, int* cu_tokens, int* slots, int* status, int R,
+                   int max_pages, int pages, int page_tokens, int tokens, int frame_tokens,
+                   int window_frames, int n_sink, cudaStream_t stream) {
+  gla::PlanParams p{lens,     held,           new_lens,  free_count, free_pages,  block_table,
+                    lens_out, held_out,       free_count_out, cu_tokens, slots, status,
+                    R,        max_pages,      pages,     page_tokens, tokens,     frame_tokens,
+                    window_frames, n_sink};
+  return cache_plan_impl(p, stream);
+}
+
+int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu_tokens,
+                    const int* slots, void* k_cache, void* v_cache, float* k_scale,
+                    float* v_scale, int* nonfinite, int R, int tokens, int Hkv, int d, int pages,
+                    int page_tokens, cudaStream_t stream) {
+  gla::StoreParams p{static_cast<const __nv_bfloat16*>(k),
+                     static_cast<const __nv_bfloat16*>(v),
+                     lens,
+                     cu_tokens,
+                     slots,
+                     static_cast<uint8_t*>(k_cache),
+                     static_cast<uint8_t*>(v_cache),
+                     k_scale,
+                     v_scale,
+                     nonfinite,
+                     R,
+                     tokens,
+                     Hkv,
+                     pages};
+  return cache_store_impl(p, d, page_tokens, stream);
+}
+
+int gla_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int* block_table,
+                        const int* lens, const int* cu_tokens, const void* gate_z, void* out,
+                        int R, int tokens, int max_new, int H, int Hkv, int d, int pages,
+                        int page_tokens, int max_pages, int frame_tokens, int window_frames,
+                        int n_sink, float scale, cudaStream_t stream) {
+  gla::CacheAttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k8 = static_cast<const uint8_t*>(k_cache);
+  p.v8 = static_cast<const uint8_t*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.table = block_table;
+  p.lens = lens;
+  p.cu = cu_tokens;
+  p.z = static_cast<const __nv_bfloat16*>(gate_z);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.R = R;
+  p.tokens = tokens;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.pages = pages;
+  p.max_pages = max_pages;
+  p.F = frame_tokens;
+  p.W = window_frames;
+  p.n_sink = n_sink;
+  return cache_attention_impl(p, max_new, d, page_tokens, scale, stream);
 }
 
 int gla_trim_workspace(void) {

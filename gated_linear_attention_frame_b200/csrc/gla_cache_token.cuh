@@ -1,0 +1,752 @@
+// gla_cache_token.cuh -- attention of a few queries a sequence (single tokens
+// and short runs) over the paged 8-bit cache.
+//
+// A query at position p of its sequence sees the keys s < min(len, (p / F + 1)
+// F) with s >= (p / F - W + 1) F or s < n_sink (W = 0: no lower bound), F the
+// frame in tokens: F = 1 is the causal form, F = tokens of a frame the anchor
+// layer's.  out = sigmoid(z) sum_s softmax_s(q . k_s scale ks) (v_s vs), ks and
+// vs the scales of the key's page.  A row that sees no key gives 0.
+//
+// With few query rows a call is bound by reading the codes once from HBM: 2 d
+// bytes a key and head.  One work unit = 16 query rows (tokens x the heads
+// that share a key/value head, padded) of one sequence and key/value head; its
+// visible keys are cut into blocks of 32.  All blocks of all units are laid
+// end to end and dealt out evenly to the CTAs, so a long sequence is split as
+// finely as the GPU is wide whatever the mix of lengths; a unit that ends up
+// in several CTAs leaves one partial (O, m, l) in each, joined in the order of
+// the keys by gla_cache_combine_kernel.
+//
+// The four warps of a CTA take every fourth block, each through its own ring
+// of cp.async stages (nothing between warps waits until a unit ends).  The
+// products run on mma.sync (m16n8k16, fp16 in, fp32 out): 16 rows would leave
+// 7/8 of a 128-row tcgen05 tile empty, and the codes reach the B fragments
+// straight from the ring, converted in registers (every e4m3 value is an fp16
+// value), with no second trip through shared memory.  The order of d inside a
+// fragment is free as long as Q uses the same one, so each thread reads 16
+// neighbouring bytes of a key; V's fragments pair two keys of one d by a byte
+// permutation.
+// Queries are scaled by a power of two per row into the top of the fp16 range
+// (exact but for elements 2^29 below the row's largest).  The value scale is
+// folded into the exponent, P' = 2^(x + log2 vs - m + kBias), and taken out
+// of the row sum again block by block.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "gla_cache.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gla {
+
+struct CacheAttnParams {
+  const __nv_bfloat16* q;
+  const uint8_t *k8, *v8;
+  const float *ks, *vs;
+  const int *table, *lens, *cu;
+  const __nv_bfloat16* z;
+  __nv_bfloat16* out;
+  int R, tokens, H, Hkv, G;  // G = H / Hkv query heads share a key/value head
+  int pages, max_pages, p_shift;  // P = 1 << p_shift
+  int F, W, n_sink;
+  float sl2;  // scale * log2(e)
+  // split units: per CTA two partials of kPartRows rows (fp32 O, then m, l)
+  // and one descriptor
+  float* part;
+  int* desc;
+};
+
+// Exponent offset of P': the largest P' of a row is about 2^kBias when its
+// reference maximum is set and may grow by 2^kLazy before the row is rescaled
+// (2^15 < 65504, the largest fp16); smaller ones keep full fp16 precision
+// down to 2^-22 of it.
+constexpr float kCacheBias = 8.0f, kCacheLazy = 7.0f;
+
+// The keys that the queries t_lo .. t_hi of one sequence see between them, as a
+// list of blocks of BK keys: the blocks of the sinks below the window, then
+// the blocks of the window.
+struct CacheSpan {
+  int lo, hi, sink;   // visible keys: [0, sink) and [lo, hi)
+  int sb, wb0, nb;    // sink blocks, first window block, blocks (at least 1)
+  __device__ __forceinline__ int pos(int k, int bk) const {
+    return (k < sb ? k : wb0 + (k - sb)) * bk;
+  }
+  __device__ __forceinline__ bool sees(int key) const {
+    return key < hi && (key >= lo || key < sink);
+  }
+};
+
+struct CacheSeq {
+  int c0, n, len;  // first packed row, new tokens, keys
+  int p0;          // position of the first new token
+};
+
+__device__ __forceinline__ CacheSeq cache_seq(const CacheAttnParams& p, int r) {
+  CacheSeq s;
+  s.c0 = min(max(p.cu[r], 0), p.tokens);
+  s.n = max(min(p.cu[r + 1], p.tokens) - s.c0, 0);
+  const int raw = max(p.lens[r], 0);
+  s.len = min(raw, p.max_pages << p.p_shift);
+  s.p0 = raw - s.n;
+  return s;
+}
+
+// Upper and lower end of the keys of a query at position pos (negative: none).
+__device__ __forceinline__ int key_hi(const CacheAttnParams& p, const CacheSeq& s, int pos) {
+  if (pos < 0) return 0;
+  const int64_t e = (static_cast<int64_t>(pos / p.F) + 1) * p.F;
+  return e < s.len ? static_cast<int>(e) : s.len;
+}
+__device__ __forceinline__ int key_lo(const CacheAttnParams& p, int pos) {
+  if (p.W == 0 || pos < 0) return 0;
+  const int64_t e = (static_cast<int64_t>(pos / p.F) - p.W + 1) * p.F;
+  return e > 0 ? static_cast<int>(e) : 0;
+}
+
+template <int BK>
+__device__ __forceinline__ CacheSpan cache_span(const CacheAttnParams& p, const CacheSeq& s,
+                                                int t_lo, int t_hi) {
+  CacheSpan v;
+  v.hi = key_hi(p, s, s.p0 + t_hi);
+  v.lo = min(key_lo(p, s.p0 + t_lo), v.hi);
+  v.sink = p.W > 0 ? min(p.n_sink, v.lo) : 0;
+  v.sb = (v.sink + BK - 1) / BK;
+  v.wb0 = max(v.lo / BK, v.sb);
+  v.nb = max(1, v.sb + max(0, (v.hi + BK - 1) / BK - v.wb0));
+  return v;
+}
+
+// Contiguous share of CTA c of `total` blocks dealt out over `ctas` CTAs.
+__device__ __forceinline__ int64_t share_lo(int64_t total, int ctas, int c) {
+  return total / ctas * c + total % ctas * c / ctas;
+}
+
+// 2^(14 - E) for a row whose largest magnitude has bf16 exponent E (zero and
+// non-finite rows: 1), as the factor and its inverse.
+__device__ __forceinline__ void row_scale(uint32_t amax_bits, float& f, float& inv) {
+  const int e = static_cast<int>(amax_bits >> 7);
+  const int up = (e == 0 || e == 255) ? 0 : 14 - (e - 127);  // in [-113, 140]
+  const int c = up > 126 ? 126 : up;
+  f = exp2_int(c);
+  inv = exp2_int(-c);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;  // 0: the 16 bytes become zero
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D (16 x 8 fp32) += A (16 x 16 fp16) B (16 x 8 fp16).
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct TokenCfg {
+  static constexpr int kThreads = 128;
+  static constexpr int kWarps = 4;
+  static constexpr int kRows = 16;
+  static constexpr int BK = 32;           // keys of a block
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kTensorBytes = BK * D;            // K or V codes of a block
+  static constexpr int kStageBytes = 2 * kTensorBytes + 16;  // + ks, vs of its two key halves
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kMergeBytes = 2 * 8 * D * 4;  // two warps' rows, eight at a time
+  static constexpr int kStatBytes = kWarps * kRows * 8;
+  static constexpr int kFixedBytes = kRingBytes + kMergeBytes + kStatBytes;
+  static constexpr int kPartFloats = kRows * D + 2 * kRows;
+  static constexpr int kCtasPerSm = 2;
+  static constexpr int kMinBlocks = 8;    // least blocks of a CTA
+  static constexpr int kChunks = D / 16;  // 16-byte chunks of a key
+};
+
+template <int D>
+__global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttnParams p) {
+  using C = TokenCfg<D>;
+  constexpr int BK = C::BK;
+  constexpr int KI = D / 64;   // 16-byte chunks of a key that one thread reads
+  constexpr int NT = D / 8;    // n-tiles of the output
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* s_o = reinterpret_cast<float*>(smem + C::kRingBytes);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kMergeBytes);
+  long long* s_pre = reinterpret_cast<long long*>(smem + C::kFixedBytes);  // [R + 1]
+  __shared__ long long scratch[33];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int P = 1 << p.p_shift;
+
+  // rows of a sequence in tiles of 16, and the blocks before each sequence
+  auto tiles_of = [&](const CacheSeq& s) {
+    return static_cast<int>((static_cast<int64_t>(s.n) * p.G + 15) >> 4);
+  };
+  auto span_of = [&](const CacheSeq& s, int tile) {
+    const int t_lo = tile * 16 / p.G;
+    const int t_hi = min(static_cast<int>((static_cast<int64_t>(tile) * 16 + 15) / p.G), s.n - 1);
+    return cache_span<BK>(p, s, t_lo, t_hi);
+  };
+  auto blocks_of = [&](int r) -> long long {
+    const CacheSeq s = cache_seq(p, r);
+    long long b = 0;
+    for (int i = 0, n = tiles_of(s); i < n; ++i) b += span_of(s, i).nb;
+    return b * p.Hkv;
+  };
+  long long total;
+  {
+    const int per = (p.R + C::kThreads - 1) / C::kThreads;
+    const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+      const long long b = blocks_of(r);
+      s_pre[r] = b;
+      sum += b;
+    }
+    long long at = block_exclusive_scan<long long>(sum, scratch, total);
+    for (int r = r0; r < r1; ++r) {
+      const long long b = s_pre[r];
+      s_pre[r] = at;
+      at += b;
+    }
+    if (tid == 0) s_pre[p.R] = total;
+    __syncthreads();
+  }
+  int* desc = p.desc + 8 * blockIdx.x;
+  const long long want = (total + C::kMinBlocks - 1) / C::kMinBlocks;
+  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  if (tid == 0) desc[0] = 0;  // nothing to join unless a unit goes on past this CTA
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long x0 = share_lo(total, ctas, blockIdx.x);
+  const long long x1 = share_lo(total, ctas, blockIdx.x + 1);
+
+  // A unit, and this warp's place in the part [k, k_end) of its blocks that
+  // belongs to this CTA.
+  struct Cursor {
+    CacheSeq s;
+    CacheSpan v;
+    int r, tile, tiles, h;
+    long long x_unit;  // block number of the unit's first block
+    int k, k0, k_end;
+    bool live;
+  };
+  auto open = [&](Cursor& c) {  // the unit's part of this CTA
+    c.v = span_of(c.s, c.tile);
+    c.k0 = c.x_unit < x0 ? static_cast<int>(x0 - c.x_unit) : 0;
+    c.k_end = c.x_unit + c.v.nb > x1 ? static_cast<int>(x1 - c.x_unit) : c.v.nb;
+    c.k = c.k0 + warp;
+  };
+  auto next_unit = [&](Cursor& c) {
+    c.x_unit += c.v.nb;
+    if (c.x_unit >= x1) {
+      c.live = false;
+      return;
+    }
+    if (++c.h == p.Hkv) {
+      c.h = 0;
+      if (++c.tile == c.tiles) {
+        c.tile = 0;
+        do {
+          ++c.r;
+          c.s = cache_seq(p, c.r);
+          c.tiles = tiles_of(c.s);
+        } while (c.tiles == 0);  // ends: blocks are left, so a sequence with rows follows
+      }
+    }
+    open(c);
+  };
+  Cursor cur;
+  {
+    cur.r = prefix_owner<long long>(s_pre, p.R, x0);
+    cur.s = cache_seq(p, cur.r);
+    cur.tiles = tiles_of(cur.s);
+    cur.x_unit = s_pre[cur.r];
+    cur.tile = 0;
+    for (;; ++cur.tile) {  // tiles are few: a sequence of this kernel has few rows
+      const int nb = span_of(cur.s, cur.tile).nb;
+      const long long all = static_cast<long long>(nb) * p.Hkv;
+      if (cur.x_unit + all > x0 || cur.tile + 1 == cur.tiles) {
+        cur.h = static_cast<int>((x0 - cur.x_unit) / nb);
+        cur.x_unit += static_cast<long long>(cur.h) * nb;
+        break;
+      }
+      cur.x_unit += all;
+    }
+    cur.live = true;
+    open(cur);
+  }
+  Cursor ld = cur;  // runs ahead: the block loaded next
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  const int64_t page_stride = static_cast<int64_t>(p.Hkv) << p.p_shift;  // rows of a page
+
+  // Start the copies of this warp's next block into stage `st`.
+  auto issue = [&](int st) {
+    while (ld.live && ld.k >= ld.k_end) next_unit(ld);
+    if (ld.live) {
+      const int base = ld.v.pos(ld.k, BK);
+      const int* row = p.table + static_cast<int64_t>(ld.r) * p.max_pages;
+      const uint32_t dst = ring + st * C::kStageBytes;
+      constexpr int kRowsPerPass = 32 / C::kChunks;  // 4 (d = 128) or 8
+      const int ch = lane % C::kChunks, rr = lane / C::kChunks;
+      // a block lies in one page, or (P = 16) each half of it in one
+      int page[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int key = base + hf * 16;
+        const int j = key >> p.p_shift;
+        int pg = j < p.max_pages ? row[j] : -1;
+        if (pg >= p.pages) pg = -1;
+        page[hf] = pg;
+      }
+#pragma unroll
+      for (int i = 0; i < BK / kRowsPerPass; ++i) {
+        const int kr = i * kRowsPerPass + rr;  // key of the block
+        const int key = base + kr;
+        const int pg = page[kr >> 4];
+        const bool ok = pg >= 0 && ld.v.sees(key);
+        const int64_t off =
+            ok ? (pg * page_stride + (static_cast<int64_t>(ld.h) << p.p_shift) + (key & (P - 1))) *
+                         D + ch * 16
+               : 0;
+        // 16-byte chunks swizzled so that the fragment reads below hit all banks
+        const int ck = D == 128 ? (ch ^ ((kr & 1) << 2)) : ch;
+        const int cv = D == 128 ? (ch ^ (((kr >> 1) & 3) << 1)) : (ch ^ ((kr >> 1) & 3));
+        cp_async16(dst + kr * D + ck * 16, p.k8 + off, ok);
+        cp_async16(dst + C::kTensorBytes + kr * D + cv * 16, p.v8 + off, ok);
+      }
+      if (lane < 4) {
+        const int hf = lane & 1;
+        const int a = base + hf * 16;  // a half that shows no key has scale 0
+        const bool any = page[hf] >= 0 && a < ld.v.hi && (a + 16 > ld.v.lo || a < ld.v.sink);
+        const float* sc = (lane < 2 ? p.ks : p.vs) +
+                          (any ? static_cast<int64_t>(page[hf]) * p.Hkv + ld.h : 0);
+        cp_async4(dst + 2 * C::kTensorBytes + lane * 4, sc, any);
+      }
+      ld.k += C::kWarps;
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s) issue(s);
+  int st = 0;
+
+  for (; cur.live; next_unit(cur)) {
+    const int rows = min(16, static_cast<int>(static_cast<int64_t>(cur.s.n) * p.G -
+                                              static_cast<int64_t>(cur.tile) * 16));
+    // ---- query fragments: rows g and g + 8 of the tile
+    uint32_t qa[D / 16][4];
+    float rs[2];                 // undoes the row scale, times scale log2(e)
+    int hi[2], lo[2];
+    int64_t qoff[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rho = g + 8 * e;
+      const bool have = rho < rows;
+      const int64_t rr = static_cast<int64_t>(cur.tile) * 16 + (have ? rho : 0);
+      const int t = static_cast<int>(rr / p.G), hq = static_cast<int>(rr % p.G);
+      qoff[e] = ((static_cast<int64_t>(cur.s.c0) + t) * p.H + cur.h * p.G + hq) * D;
+      hi[e] = have ? key_hi(p, cur.s, cur.s.p0 + t) : 0;
+      lo[e] = key_lo(p, cur.s.p0 + t);
+      uint4 w[KI][2];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          w[i][f] = make_uint4(0, 0, 0, 0);
+          if (have)
+            w[i][f] = *reinterpret_cast<const uint4*>(p.q + qoff[e] + i * 64 + t4 * 16 + f * 8);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[i][f].x & 0x7FFF7FFFu, w[i][f].y & 0x7FFF7FFFu),
+                                     __vmaxu2(w[i][f].z & 0x7FFF7FFFu, w[i][f].w & 0x7FFF7FFFu)));
+        }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      float f, inv;
+      row_scale(mx, f, inv);
+      rs[e] = inv * p.sl2;
+#pragma unroll
+      for (int i = 0; i < KI; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const uint4& x = w[i][jj >> 1];
+          const uint32_t w0 = (jj & 1) ? x.z : x.x, w1 = (jj & 1) ? x.w : x.y;
+          qa[i * 4 + jj][e] = pack_f16x2(bf16lo_to_f32(w0) * f, bf16hi_to_f32(w0) * f);
+          qa[i * 4 + jj][2 + e] = pack_f16x2(bf16lo_to_f32(w1) * f, bf16hi_to_f32(w1) * f);
+        }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // every row sees every key of a block inside [all_lo, all_hi)
+    const int all_hi = key_hi(p, cur.s, cur.s.p0 + static_cast<int>(static_cast<int64_t>(cur.tile) * 16 / p.G));
+    const int all_lo = key_lo(p, cur.s.p0 + static_cast<int>((static_cast<int64_t>(cur.tile) * 16 + rows - 1) / p.G));
+
+    for (; cur.k < cur.k_end; cur.k += C::kWarps) {
+      cp_async_wait<C::kStages - 1>();
+      __syncwarp();
+      const uint32_t kb = ring + st * C::kStageBytes, vb = kb + C::kTensorBytes;
+      const uint4 sc = ld_shared_v4(vb + C::kTensorBytes);
+      const float ksc[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
+      const float vsc[2] = {__uint_as_float(sc.z), __uint_as_float(sc.w)};
+      // ---- S = Q K^T: 16 rows x 32 keys
+      float s[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        const int kr = j * 8 + g;
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+          const int c = i * 4 + t4;
+          const uint4 w = ld_shared_v4(kb + kr * D + (D == 128 ? (c ^ ((kr & 1) << 2)) : c) * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj)
+            mma_f16_16816(s[j], qa[i * 4 + jj], e4m3x2_to_f16x2(ww[jj] & 0xFFFFu),
+                          e4m3x2_to_f16x2(ww[jj] >> 16));
+        }
+      }
+      const int base = cur.v.pos(cur.k, BK);
+      float lv[2], iv[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        lv[hf] = lg2_approx(vsc[hf]);  // scale 0 (nothing visible): -inf
+        iv[hf] = vsc[hf] > 0.f ? ex2_approx(-lv[hf]) : 0.f;
+      }
+      const bool whole = base >= all_lo && base + BK <= all_hi;  // uniform
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int e = x >> 1;
+          s[j][x] = fmaf(s[j][x], rs[e] * ksc[j >> 1], lv[j >> 1]);
+          if (!whole) {
+            const int key = base + j * 8 + t4 * 2 + (x & 1);
+            if (!(key < hi[e] && (key >= lo[e] || key < p.n_sink))) s[j][x] = -INFINITY;
+          }
+        }
+      bool grow = false;
+      float mt[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float a = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = fmax3(a, s[j][2 * e], s[j][2 * e + 1]);
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        mt[e] = a;
+        grow |= a > m[e] + kCacheLazy || (m[e] == -INFINITY && a != -INFINITY);
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[e], mt[e]);
+          const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mn);
+          m[e] = mn;
+          l[e] *= f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][2 * e] *= f;
+            o[n][2 * e + 1] *= f;
+          }
+        }
+      }
+      // ---- P' and the row sums (the value scale leaves the sums again)
+      uint32_t pa[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float sh = m[e] == -INFINITY ? 0.f : kCacheBias - m[e];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          float x[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) x[y] = ex2_approx(s[hf * 2 + (y >> 1)][2 * e + (y & 1)] + sh);
+          l[e] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv[hf], l[e]);
+          pa[hf][e] = pack_f16x2(x[0], x[1]);
+          pa[hf][2 + e] = pack_f16x2(x[2], x[3]);
+        }
+      }
+      // ---- O += P' V
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if constexpr (D == 128) {
+          uint4 w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int kr = hf * 16 + t4 * 2 + (y & 1) + (y >> 1) * 8;
+            w[y] = ld_shared_v4(vb + kr * D + ((g ^ (((kr >> 1) & 3) << 1))) * 16);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t a0 = (&w[0].x)[q], a1 = (&w[1].x)[q], a2 = (&w[2].x)[q],
+                           a3 = (&w[3].x)[q];
+            const uint32_t b0 = __byte_perm(a0, a1, 0x5140), b1 = __byte_perm(a2, a3, 0x5140);
+            const uint32_t c0 = __byte_perm(a0, a1, 0x7362), c1 = __byte_perm(a2, a3, 0x7362);
+            mma_f16_16816(o[q * 4 + 0], pa[hf], e4m3x2_to_f16x2(b0 & 0xFFFFu),
+                          e4m3x2_to_f16x2(b1 & 0xFFFFu));
+            mma_f16_16816(o[q * 4 + 1], pa[hf], e4m3x2_to_f16x2(b0 >> 16),
+                          e4m3x2_to_f16x2(b1 >> 16));
+            mma_f16_16816(o[q * 4 + 2], pa[hf], e4m3x2_to_f16x2(c0 & 0xFFFFu),
+                          e4m3x2_to_f16x2(c1 & 0xFFFFu));
+            mma_f16_16816(o[q * 4 + 3], pa[hf], e4m3x2_to_f16x2(c0 >> 16),
+                          e4m3x2_to_f16x2(c1 >> 16));
+          }
+        } else {
+          uint2 w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int kr = hf * 16 + t4 * 2 + (y & 1) + (y >> 1) * 8;
+            const uint32_t ad = vb + kr * D + (((g >> 1) ^ ((kr >> 1) & 3)) * 16) + (g & 1) * 8;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                         : "=r"(w[y].x), "=r"(w[y].y)
+                         : "r"(ad)
+                         : "memory");
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t a0 = q ? w[0].y : w[0].x, a1 = q ? w[1].y : w[1].x,
+                           a2 = q ? w[2].y : w[2].x, a3 = q ? w[3].y : w[3].x;
+            const uint32_t b0 = __byte_perm(a0, a1, 0x5140), b1 = __byte_perm(a2, a3, 0x5140);
+            const uint32_t c0 = __byte_perm(a0, a1, 0x7362), c1 = __byte_perm(a2, a3, 0x7362);
+            mma_f16_16816(o[q * 4 + 0], pa[hf], e4m3x2_to_f16x2(b0 & 0xFFFFu),
+                          e4m3x2_to_f16x2(b1 & 0xFFFFu));
+            mma_f16_16816(o[q * 4 + 1], pa[hf], e4m3x2_to_f16x2(b0 >> 16),
+                          e4m3x2_to_f16x2(b1 >> 16));
+            mma_f16_16816(o[q * 4 + 2], pa[hf], e4m3x2_to_f16x2(c0 & 0xFFFFu),
+                          e4m3x2_to_f16x2(c1 & 0xFFFFu));
+            mma_f16_16816(o[q * 4 + 3], pa[hf], e4m3x2_to_f16x2(c0 >> 16),
+                          e4m3x2_to_f16x2(c1 >> 16));
+          }
+        }
+      }
+      __syncwarp();  // the stage is read by every lane before it is loaded again
+      issue(st);
+      st = st + 1 == C::kStages ? 0 : st + 1;
+    }
+
+    // ---- join the four warps.  Thread (g, t4) holds rows g, g + 8 and the
+    // columns D / 4 t4 .. + D / 4 - 1 (n-tile n: columns n and D / 8 + n of them).
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (t4 == 0) s_ml[warp * 16 + g + 8 * e] = make_float2(m[e], l[e]);
+    }
+    __syncthreads();
+    float mm[2], ll[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float2 a[C::kWarps];
+      mm[e] = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) {
+        a[w] = s_ml[w * 16 + g + 8 * e];
+        mm[e] = fmaxf(mm[e], a[w].x);
+      }
+      ll[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w)
+        ll[e] += a[w].x == -INFINITY ? 0.f : a[w].y * ex2_approx(a[w].x - mm[e]);
+      const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mm[e]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        o[n][2 * e] *= f;
+        o[n][2 * e + 1] *= f;
+      }
+    }
+    const bool low = rows > 8;  // rows g + 8 hold something (uniform)
+    auto slot = [&](int buf, int n, int x) -> float& {
+      return s_o[((buf * 2 * NT) + n * 2 + x) * 32 + lane];
+    };
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // rows g, then rows g + 8
+      if (e == 1) {
+        if (!low) break;
+        __syncthreads();  // the buffers are read
+      }
+#pragma unroll
+      for (int half = 2; half >= 1; half >>= 1) {  // warps half .. 2 half - 1 give, the others take
+        if (warp >= half && warp < 2 * half) {
+          const int buf = half == 2 ? warp - 2 : 1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            slot(buf, n, 0) = o[n][2 * e];
+            slot(buf, n, 1) = o[n][2 * e + 1];
+          }
+        }
+        __syncthreads();
+        if (warp < half) {
+          const int buf = half == 2 ? warp : 1;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][2 * e] += slot(buf, n, 0);
+            o[n][2 * e + 1] += slot(buf, n, 1);
+          }
+        }
+      }
+    }
+    const bool starts = cur.k0 == 0, ends = cur.k_end == cur.v.nb;
+    if (warp == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rho = g + 8 * e;
+        if (rho >= rows) continue;
+        constexpr int kCols = D / 4;  // columns of this thread
+        if (starts && ends) {
+          const float rl = mm[e] == -INFINITY ? 0.f : 1.0f / ll[e];
+          __nv_bfloat16* dst = p.out + qoff[e] + t4 * kCols;
+          const __nv_bfloat16* zs = p.z != nullptr ? p.z + qoff[e] + t4 * kCols : nullptr;
+#pragma unroll
+          for (int c = 0; c < kCols / 8; ++c) {
+            float x[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const int col = c * 8 + y;  // column col of the thread: n-tile col % NT
+              x[y] = o[col % NT][2 * e + col / NT] * rl;
+            }
+            if (zs != nullptr) {
+              const uint4 zw = *reinterpret_cast<const uint4*>(zs + c * 8);
+              const uint32_t zz[4] = {zw.x, zw.y, zw.z, zw.w};
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const float zf =
+                    (y & 1) ? bf16hi_to_f32(zz[y >> 1]) : bf16lo_to_f32(zz[y >> 1]);
+                x[y] *= 1.0f / (1.0f + expf(-zf));
+              }
+            }
+            *reinterpret_cast<uint4*>(dst + c * 8) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          }
+        } else {
+          // the CTA's first part of a unit begun before it goes to its
+          // partial 0, a unit that goes on after it to partial 1
+          float* part = p.part + (2ll * blockIdx.x + (starts ? 1 : 0)) * C::kPartFloats;
+          float* dst = part + rho * D + t4 * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 4)
+            *reinterpret_cast<float4*>(dst + c) =
+                make_float4(o[c % NT][2 * e + c / NT], o[(c + 1) % NT][2 * e + (c + 1) / NT],
+                            o[(c + 2) % NT][2 * e + (c + 2) / NT],
+                            o[(c + 3) % NT][2 * e + (c + 3) / NT]);
+          if (t4 == 0)
+            *reinterpret_cast<float2*>(part + 16 * D + 2 * rho) = make_float2(mm[e], ll[e]);
+        }
+      }
+      if (lane == 0 && starts && !ends) {
+        int parts = 1;
+        const long long x_end = cur.x_unit + cur.v.nb;
+        for (int c = blockIdx.x + 1; c < ctas && share_lo(total, ctas, c) < x_end; ++c) ++parts;
+        desc[1] = cur.s.c0;
+        desc[2] = cur.tile * 16;
+        desc[3] = cur.h;
+        desc[4] = rows;
+        desc[0] = parts;
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+// Joins the partials of a unit that several CTAs share: CTA x of the grid takes
+// the unit (if any) that begins in CTA x of the attention kernel and goes on
+// after it; its parts are partial 1 of that CTA and partial 0 of the next
+// ones.  blockIdx.y: a query row.  Four (eight at d = 64) groups of threads
+// take every fourth (eighth) part; the sums are joined in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnParams p,
+                                                                int part_floats, int part_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kGroups = 128 / (D / 4);
+  __shared__ float4 s_acc[128];
+  __shared__ float s_m[kGroups], s_l[kGroups];
+  const int* desc = p.desc + 8 * blockIdx.x;
+  const int parts = desc[0], rho = blockIdx.y;
+  if (parts == 0 || rho >= desc[4]) return;
+  const int grp = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
+  auto part_of = [&](int i) {
+    return p.part + (i == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + i)) * part_floats;
+  };
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = grp; i < parts; i += kGroups) {
+    const float* a = part_of(i);
+    const float2 ml = *reinterpret_cast<const float2*>(a + part_rows * D + 2 * rho);
+    if (ml.x == -INFINITY) continue;  // uniform over the group
+    const float4 x = *reinterpret_cast<const float4*>(a + rho * D + c4 * 4);
+    const float mn = fmaxf(m, ml.x);
+    const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn), f1 = exp2f(ml.x - mn);
+    m = mn;
+    l = l * f0 + ml.y * f1;
+    acc.x = acc.x * f0 + x.x * f1;
+    acc.y = acc.y * f0 + x.y * f1;
+    acc.z = acc.z * f0 + x.z * f1;
+    acc.w = acc.w * f0 + x.w * f1;
+  }
+  s_acc[threadIdx.x] = acc;
+  if (c4 == 0) {
+    s_m[grp] = m;
+    s_l[grp] = l;
+  }
+  __syncthreads();
+  if (grp != 0) return;
+  float mm = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) mm = fmaxf(mm, s_m[i]);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float f = s_m[i] == -INFINITY ? 0.f : exp2f(s_m[i] - mm);
+    const float4 x = s_acc[i * (D / 4) + c4];
+    l += s_l[i] * f;
+    o.x += x.x * f;
+    o.y += x.y * f;
+    o.z += x.z * f;
+    o.w += x.w * f;
+  }
+  const float rl = mm == -INFINITY ? 0.f : 1.0f / l;
+  const int row = desc[2] + rho;
+  const int64_t off =
+      ((static_cast<int64_t>(desc[1]) + row / p.G) * p.H + desc[3] * p.G + row % p.G) * D + c4 * 4;
+  float x[4] = {o.x * rl, o.y * rl, o.z * rl, o.w * rl};
+  if (p.z != nullptr) {
+    const uint2 zw = *reinterpret_cast<const uint2*>(p.z + off);
+    const float zf[4] = {bf16lo_to_f32(zw.x), bf16hi_to_f32(zw.x), bf16lo_to_f32(zw.y),
+                         bf16hi_to_f32(zw.y)};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) x[y] *= 1.0f / (1.0f + expf(-zf[y]));
+  }
+  *reinterpret_cast<uint2*>(p.out + off) =
+      make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+
+}  // namespace gla

@@ -213,6 +213,131 @@ int gla_softmax_anchor_step(const void* q, const void* k, const void* v, const v
                             cudaStream_t stream);
 
 /*
+ * The paged 8-bit rollout cache of the softmax anchor layers.
+ *
+ * The SANA-WM pages (method components) keep the softmax layers' memory and
+ * per-chunk latency constant over long rollouts with attention sinks and a
+ * local window of frames; the SANA-Video talk (block KV cache) reuses what
+ * earlier blocks left behind.  gla_softmax_anchor_step does that for one batch
+ * of equal rollouts from bf16 caches that its caller copies together.  These
+ * three entry points serve many sequences of different lengths at once: the
+ * keys and values live in pages of a shared pool, in 8 bits, and pages that
+ * no later query can see go back to the pool.  One step of a serving loop is
+ * plan, then (for each layer) store and attention, all on one stream, with no
+ * host synchronisation.  The pages give no formulas for any of this; the
+ * definitions are below.
+ *
+ *   P = page_tokens  16, 32, 64 or 128 tokens of one sequence in a page
+ *   F = frame_tokens a query sees its whole frame: F = 1 is causal attention
+ *                    token by token, F = tokens of a latent frame the anchor
+ *                    layer's mask
+ *   W = window_frames  frames a query sees, its own included; 0: all
+ *   n_sink           the first n_sink tokens of a sequence stay visible
+ *   d                head dim, 64 or 128
+ *   R                sequences of the call, at most 8192
+ *   tokens           rows of the packed token arrays.  The new tokens of
+ *                    sequence r are rows cu_tokens[r] .. cu_tokens[r+1] - 1;
+ *                    rows from cu_tokens[R] on belong to nobody and are
+ *                    neither read nor written.
+ *   caches           e4m3 codes [pages, Hkv, P, d]; scales fp32 [pages, Hkv],
+ *                    powers of two; a value is code * scale.
+ *   block_table      int32 [R, max_pages]: entry j of row r is the page of
+ *                    tokens j P .. j P + P - 1.  Entries that no visible token
+ *                    needs may hold anything; a key whose entry is not in 0 ..
+ *                    pages - 1 is not attended.
+ * pages * P and max_pages * P must stay below 2^31 (slots are 32-bit).  Integer
+ * arrays and scales are 4-byte aligned, the others 16-byte aligned.
+ */
+
+/*
+ * gla_cache_plan -- the lengths, pages and slots of one step, on the GPU.
+ *
+ * Per sequence r with L = lens[r] cached tokens and n = new_lens[r] new ones:
+ *   n < 0   the sequence has ended: all its pages go back, its length is 0.
+ *   else    with w_lo = max(0, (L / F - W + 1) F) (W > 0), the lower end of the
+ *           window of the next token, the pages max(ceil(n_sink / P), held[r])
+ *           .. w_lo / P - 1 go back (held[r]: first page behind the sinks that
+ *           is still held; held_out = max(held, w_lo / P)), and ceil((L + n) /
+ *           P) - ceil(L / P) new pages are appended.
+ * free_pages [pages] is a stack with free_count[0] entries: returned pages are
+ * pushed in the order of (sequence, page), then the new pages are popped, the
+ * first pop for the first new page of the first sequence; so a page may be
+ * returned and taken in one step.  Outputs: lens_out = L + n, held_out,
+ * free_count_out, cu_tokens [R + 1], slots [tokens] = page * P + offset of every
+ * new token (-1 behind the last), the new entries of block_table (returned
+ * entries keep their old value), and status[0]:
+ *   0  done
+ *   1  not enough pages     2  more new tokens than `tokens`
+ *   4  a sequence needs more than max_pages pages
+ *   8  free_count is negative, or more pages would be free than there are
+ * (bits add up).  With a nonzero status nothing changes: lens_out, held_out and
+ * free_count_out equal their inputs, cu_tokens is 0 and slots are -1, so that
+ * a store and an attention behind it do nothing.
+ * lens_out, held_out and free_count_out may be the inputs' pointers.  The call
+ * is one kernel, takes no workspace and may be captured into a CUDA graph.
+ */
+int gla_cache_plan(const int* lens, const int* held, const int* new_lens, const int* free_count,
+                   int* free_pages, int* block_table, int* lens_out, int* held_out,
+                   int* free_count_out, int* cu_tokens, int* slots, int* status, int R,
+                   int max_pages, int pages, int page_tokens, int tokens, int frame_tokens,
+                   int window_frames, int n_sink, cudaStream_t stream);
+
+/*
+ * gla_cache_store -- quantise the new tokens' keys and values into the cache.
+ *
+ *   k, v    bf16 [tokens, Hkv, d];  lens [R] lengths AFTER the step, cu_tokens
+ *           and slots as gla_cache_plan writes them.
+ * For each page, head and tensor that receives tokens, with a = the largest
+ * finite |x| among them: scale = the smallest power of two (2^-60 .. 2^60) with
+ * a <= 448 scale, and, if the page holds earlier tokens of the sequence (the
+ * first slot is not the page's first), not below the page's scale before.
+ * New codes are x / scale rounded to the nearest e4m3 value (ties to even),
+ * saturating at +-448; infinities saturate too and NaN is stored as 0.  If the
+ * page's scale grew, its earlier codes are rounded again to the new one (exact
+ * but for codes that become subnormal).  The tokens of one sequence that fall
+ * into one page take consecutive slots.  A run of tokens whose first slot is
+ * outside 0 .. pages * P - 1 is skipped.
+ *   nonfinite  int32 counter, or NULL: the number of NaN and infinite elements
+ *              met is added to it.
+ * One kernel, no workspace.  A call with no work returns GLA_OK.
+ */
+int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu_tokens,
+                    const int* slots, void* k_cache, void* v_cache, float* k_scale,
+                    float* v_scale, int* nonfinite, int R, int tokens, int Hkv, int d, int pages,
+                    int page_tokens, cudaStream_t stream);
+
+/*
+ * gla_cache_attention -- softmax attention of the new tokens over the cache.
+ *
+ *   q, out  bf16 [tokens, H, d], H a multiple of Hkv with H / Hkv <= 128: query
+ *           head h reads key/value head h / (H / Hkv).  out must not overlap
+ *           the inputs.
+ *   gate_z  bf16 [tokens, H, d] or NULL.
+ *   lens    [R] keys of each sequence (after the step); the queries of r are its
+ *           last cu_tokens[r+1] - cu_tokens[r] positions.
+ * A query at position p sees the keys s < min(lens[r], (p / F + 1) F) with
+ * s >= (p / F - W + 1) F (any s if W = 0) or s < n_sink, and
+ *   out = sigmoid(gate_z) * sum_s softmax_s(scale q . k_s) v_s;
+ * a query that sees no key gives 0.  Codes 0x7f and 0xff (the e4m3 NaN, which
+ * gla_cache_store never writes) must not stand in a visible slot; slots behind
+ * a sequence's end may hold anything.
+ *   max_new  the largest number of new tokens of one sequence, as far as the
+ *            host knows it: it picks the kernel, not the result's range.
+ *   scale    score scale, > 0 and finite (1 / sqrt(d) for the anchor layer).
+ * Precision: e4m3 codes enter the products exactly, q scaled by a power of two
+ * per row (exact), the softmax weights rounded to fp16; scores, sums and
+ * outputs accumulate in fp32, out is rounded once to bf16.  The same inputs
+ * give the same bits.
+ * Memory: a workspace from the library's pool, freed on `stream`.
+ */
+int gla_cache_attention(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int* block_table,
+                        const int* lens, const int* cu_tokens, const void* gate_z, void* out,
+                        int R, int tokens, int max_new, int H, int Hkv, int d, int pages,
+                        int page_tokens, int max_pages, int frame_tokens, int window_frames,
+                        int n_sink, float scale, cudaStream_t stream);
+
+/*
  * gla_forward_gdn -- the frame-wise gated delta-rule variant (Gated DeltaNet).
  *
  * The SANA-WM pages (paper analysis: abstract, method components) describe
