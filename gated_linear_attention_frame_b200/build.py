@@ -23,7 +23,7 @@ DEPENDS = SOURCES + [
     for n in ("sm100_ptx.cuh", "gla_common.cuh", "gla_increment.cuh", "gla_scan.cuh",
               "gla_output.cuh", "gla_bwd_q.cuh", "gla_scan_bwd.cuh", "gla_bwd_kv.cuh",
               "gla_rope.cuh", "gla_gdn_scan.cuh", "gla_softmax_anchor.cuh", "gla_cache.cuh",
-              "gla_cache_token.cuh")
+              "gla_cache_token.cuh", "gla_cache_frame.cuh")
 ] + [os.path.join(INCLUDE, "gla.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]

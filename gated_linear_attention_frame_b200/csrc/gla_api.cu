@@ -38,6 +38,7 @@
 #include "gla_bwd_kv.cuh"
 #include "gla_bwd_q.cuh"
 #include "gla_cache.cuh"
+#include "gla_cache_frame.cuh"
 #include "gla_cache_token.cuh"
 #include "gla_common.cuh"
 #include "gla_gdn_scan.cuh"
@@ -198,9 +199,24 @@ cudaError_t set_cache_attrs() {
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            gla::TokenCfg<64>::kFixedBytes + kPre);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(gla::gla_cache_token_kernel<128>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              gla::TokenCfg<128>::kFixedBytes + kPre);
+  e = cudaFuncSetAttribute(gla::gla_cache_token_kernel<128>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gla::TokenCfg<128>::kFixedBytes + kPre);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gla::gla_cache_frame_kernel<64>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gla::FrameCfg<64>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gla::gla_cache_frame_kernel<128>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           gla::FrameCfg<128>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  constexpr int kSchedule = 160 * 1024;
+  e = cudaFuncSetAttribute(gla::gla_cache_schedule_kernel<64>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedule);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gla::gla_cache_schedule_kernel<128>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSchedule);
 }
 
 // Per-device one-time set-up: SM count, architecture check, kernel attributes,
@@ -1055,6 +1071,30 @@ int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t strea
   return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
+// Shared memory of the schedule kernel's prefix sums; longer ones go to the
+// workspace.
+constexpr size_t kScheduleSmem = 160 * 1024;
+
+template <int D>
+int launch_combine(const gla::CacheAttnParams& p, int ctas, int part_floats, int rows,
+                   int half_rows, int used, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, rows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p, part_floats, rows, half_rows,
+                         used) != cudaSuccess) {
+    cudaGetLastError();
+    return GLA_ERR_LAUNCH;
+  }
+  return GLA_OK;
+}
+
 template <int D>
 int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t stream) {
   using C = gla::TokenCfg<D>;
@@ -1070,21 +1110,51 @@ int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
   gla::gla_cache_token_kernel<D><<<grid, C::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) status = GLA_ERR_LAUNCH;
   if (status == GLA_OK) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, C::kRows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p, int(C::kPartFloats),
-                           int(C::kRows)) != cudaSuccess) {
-      cudaGetLastError();
-      status = GLA_ERR_LAUNCH;
-    }
+    status = launch_combine<D>(p, grid, C::kPartFloats, C::kRows, C::kRows, C::kRows, stream);
   }
+  if (cudaFreeAsync(ws, stream) != cudaSuccess) {
+    cudaGetLastError();
+    if (status == GLA_OK) status = GLA_ERR_LAUNCH;
+  }
+  return status;
+}
+
+template <int D>
+int run_cache_frame(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t stream) {
+  using C = gla::FrameCfg<D>;
+  gla::FrameSchedule fs{};
+  fs.ctas = di.sms;
+  fs.TQ = 128 / p.G;
+  fs.entries_max = p.tokens / (2 * fs.TQ) + p.R;
+  const size_t e0_bytes = (static_cast<size_t>(p.R + 1) * 4 + 15) / 16 * 16;
+  const size_t pre_bytes = (static_cast<size_t>(fs.entries_max) + 1) * 8;
+  fs.use_smem = e0_bytes + pre_bytes <= kScheduleSmem;
+  const int64_t starts_bytes = align256(static_cast<int64_t>(fs.ctas) * 16);
+  const int64_t n_bytes = align256(static_cast<int64_t>(fs.ctas) * 4);
+  const int64_t desc_bytes = align256(static_cast<int64_t>(fs.ctas) * 32);
+  const int64_t gpre_bytes = fs.use_smem ? 0 : align256(static_cast<int64_t>(pre_bytes));
+  const int64_t part_bytes = static_cast<int64_t>(fs.ctas) * 2 * C::kPartFloats * 4;
+  uint8_t* ws = nullptr;
+  int status = take_workspace(starts_bytes + n_bytes + desc_bytes + gpre_bytes + part_bytes,
+                              stream, &ws);
+  if (status != GLA_OK) return status;
+  fs.starts = reinterpret_cast<int4*>(ws);
+  fs.n = reinterpret_cast<int*>(ws + starts_bytes);
+  p.desc = reinterpret_cast<int*>(ws + starts_bytes + n_bytes);
+  fs.prefix = reinterpret_cast<long long*>(ws + starts_bytes + n_bytes + desc_bytes);
+  p.part = reinterpret_cast<float*>(ws + starts_bytes + n_bytes + desc_bytes + gpre_bytes);
+  gla::gla_cache_schedule_kernel<D>
+      <<<1, 1024, e0_bytes + (fs.use_smem ? pre_bytes : 0), stream>>>(p, fs);
+  if (cudaGetLastError() != cudaSuccess) status = GLA_ERR_LAUNCH;
+  if (status == GLA_OK &&
+      launch_dependent(gla::gla_cache_frame_kernel<D>, static_cast<unsigned>(fs.ctas),
+                       static_cast<unsigned>(C::kThreads), C::kSmemBytes, stream, p,
+                       fs) != cudaSuccess) {
+    cudaGetLastError();
+    status = GLA_ERR_LAUNCH;
+  }
+  if (status == GLA_OK)
+    status = launch_combine<D>(p, fs.ctas, C::kPartFloats, C::kRows, 128, fs.TQ * p.G, stream);
   if (cudaFreeAsync(ws, stream) != cudaSuccess) {
     cudaGetLastError();
     if (status == GLA_OK) status = GLA_ERR_LAUNCH;
@@ -1122,7 +1192,11 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;
-  return d == 64 ? run_cache_token<64>(p, di, stream) : run_cache_token<128>(p, di, stream);
+  // up to 64 query rows of a sequence and head: the keys are read (row tiles)
+  // times; more fill the 128-row tiles of the tensor cores
+  if (static_cast<int64_t>(max_new) * p.G <= 64)
+    return d == 64 ? run_cache_token<64>(p, di, stream) : run_cache_token<128>(p, di, stream);
+  return d == 64 ? run_cache_frame<64>(p, di, stream) : run_cache_frame<128>(p, di, stream);
 }
 
 }  // namespace

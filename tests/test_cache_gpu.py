@@ -273,7 +273,7 @@ def test_attention_follows_the_oracle(gla, case):
         c.step(gla, old, bf((sum(old), Hkv, d), case, 1), bf((sum(old), Hkv, d), case + 50, 2))
     c.step(gla, new, bf((sum(new), Hkv, d), case + 7, 1), bf((sum(new), Hkv, d), case + 77, 2))
     outs = [check_attention(gla, c, new, Hkv * G, F, W, sink, gate, 900 + case, max_new=m)
-            for m in (max(new), sum(new) + 2, 1)]  # the hint never changes what is computed
+            for m in (max(new), 1 << 20, 1)]  # the hint never changes what is computed
     assert torch.allclose(outs[0].float(), outs[1].float(), rtol=2 ** -6, atol=2 ** -6)
 
 
