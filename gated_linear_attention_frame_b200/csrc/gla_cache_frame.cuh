@@ -13,27 +13,31 @@
 //
 // Both halves of a unit share each key/value tile, because every tile has to
 // be converted first: tcgen05 wants both operands of a product in one type,
-// and q in 8 bits would cost its precision.  Four converter warps read the
-// codes from global memory straight into registers (one tile ahead), turn
-// them into fp16 (exact) and write them in the swizzled operand layout; the
-// mask's outer ends are handled there too (keys that no row of the unit sees
-// become zeros), so stray pages and NaN codes never reach a product.
+// and q in 8 bits would cost its precision.  A producer warp brings the codes
+// in by bulk copies (a page of one head is contiguous), four converter warps
+// turn them into fp16 and write them in the swizzled operand layout.  All 128
+// keys of a tile take one key scale and one value scale, the largest of its
+// pages': the converters multiply the codes of the other pages by the ratio, a
+// power of two (exact while it is at least 2^-15; beyond, below 2^-33 of the
+// largest value).  Keys that no row of the unit sees become zeros there, so
+// stray pages and NaN codes never reach a product.
 //   S_h = Q_h K^T   A = Q half [128 x d] K-major, B = K tile [128 keys] K-major
 //   O_h += P_h V    A = P_h in TMEM (fp16, over the columns of S_h),
 //                   B = V tile [128 keys x d] MN-major
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).  One issuing
-// warp per half: P V of tile j, then S of tile j + 1 into the same columns
-// (the tensor core runs one thread's products in order), while the other
-// half's softmax runs; so the two halves alternate between the tensor core and
-// the exponentials.
-// Softmax: one thread per row.  x = S f_g + lv_g for the keys of 16-key group
-// g (f_g: key scale x row scale x softmax scale x log2 e, lv_g: log2 of the
-// value scale), P' = 2^(x - m + kCacheBias); the row's reference maximum m
-// moves only when a tile exceeds it by 2^kCacheLazy, and O is rescaled then.
-// One pair of exponentials in four runs on the FMA pipe (exp2_poly3_x2).
+// warp per half: P V of tile j, then S of tile j + 1 into the same columns (the tensor core runs one thread's
+// products in order), while the other half's softmax runs; so the two halves
+// alternate between the tensor core and the exponentials.
+// Softmax: one thread per row.  P' = 2^(S f + lv - m + kCacheBias), f = key scale
+// x row scale x softmax scale x log2 e, lv = log2 of the value scale (taken out
+// of the row sum again).  The maximum of a tile is not taken as a rule: the
+// row's reference m stays while the sum of P' over 64 keys stays below 2^15
+// (then no P' leaves the fp16 range); otherwise, and on the first keys that a
+// row sees, they are read again, m becomes their maximum, and O is rescaled.  One pair of exponentials in four runs on the FMA pipe
+// (exp2_poly3_x2).
 // Warp roles: 0-3 / 4-7 softmax and epilogue of half 0 / 1, 8-11 converters,
-// 12 / 13 MMA issuers of half 0 / 1 (14, 15 idle: they complete a register
-// group).
+// 12 / 13 MMA issuers of half 0 / 1, 14 producer (15 idle: it completes the
+// register group).
 #pragma once
 
 #include "gla_cache_token.cuh"
@@ -58,6 +62,122 @@ __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// mbar_wait with a suspend hint: a waiting warp leaves the issue slots to the
+// others for up to 20 us at a time instead of polling.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               unsigned int code) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;  // up to 16 tries
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 c;\n\t"
+        "mov.u32 c, 0;\n\t"
+        "TRY_%=:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE_%=;\n\t"
+        "add.u32 c, c, 1;\n\t"
+        "setp.lt.u32 q, c, 16;\n\t"
+        "@q bra TRY_%=;\n\t"
+        "DONE_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > g_gla_wait_limit_ns) {
+      *abort = 1;
+      atomicOr(&g_gla_fault, code);
+      return false;
+    }
+  }
+}
+
+// The same for every lane of a warp (each lane acquires by its own wait).
+__device__ __forceinline__ bool warp_wait_idle(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               unsigned int code) {
+  const bool ok = mbar_wait_idle(bar, parity, abort, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// tcgen05.wait::ld that the registers of the load depend on: nothing that uses
+// them can be moved before it.
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// i / G for 0 <= i < 256 and 1 <= G <= 128, with m = (65536 + G - 1) / G (checked
+// for every i and G).
+__device__ __forceinline__ int small_div(int i, int m) { return (i * m) >> 16; }
+
+// 32-byte global accesses, a whole sector for each lane.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// Which of the 32 keys from `key` on a row sees: [lo, hi) and the sinks, without
+// the 16-key groups of bad (two bits).
+__device__ __forceinline__ uint32_t visible_bits(int key, int lo, int hi, int n_sink,
+                                                 uint32_t bad) {
+  const uint32_t w = bits_below(hi - key) & (~bits_below(lo - key) | bits_below(n_sink - key));
+  return w & ~((bad & 1u ? 0xFFFFu : 0u) | (bad & 2u ? 0xFFFF0000u : 0u));
+}
+
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t visible) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(visible >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
+}
+
+// What the producer leaves about a tile and about a segment (a CTA's tiles of
+// one unit), so that no other warp has to walk the schedule: registers are what
+// the softmax and the converters have least of, and a spilled one costs a trip
+// to L2 here (shared memory takes nearly all of L1).
+struct TileInfo {
+  uint32_t kfac[8], vfac[8];  // fp16 pair: scale of each 16-key group over the tile's
+  float ks, lv, iv;           // key scale; log2 of the value scale and 2^-lv
+  uint32_t flags;
+  int base;                   // position of the first key
+  uint32_t pad[3];
+};
+static_assert(sizeof(TileInfo) == 96, "one slot of the info ring");
+enum : uint32_t {
+  kTileBad = 255u,     // bit g: 16-key group g has no page
+  kTileAll = 256u,     // every key of the tile is visible to some row
+  kTileScaleK = 512u,  // the factors of K (V) are not all 1
+  kTileScaleV = 1024u,
+  kTileFirst = 2048u,  // first, last tile of its segment
+  kTileLast = 4096u,
+};
+struct SegInfo {
+  long long row0;    // (first token of the unit) * H + (first query head): row of q and out
+  int tokens;        // tokens of the unit (at most 2 TQ count)
+  int p0;            // position of its first token
+  int len;           // keys of the sequence
+  int lo, hi, sink;  // visible keys, as in CacheSpan
+  int whole, starts; // the segment is the unit; it holds the unit's first tile
+  int c0, unit_row, h, rest;  // for the join: first packed row, first row, head, tiles after
+};
+static_assert(sizeof(SegInfo) == 56, "one slot of the segment ring");
+
 template <int D>
 struct FrameCfg {
   using G = Geo<D>;
@@ -66,21 +186,24 @@ struct FrameCfg {
   static constexpr int kRows = 256;
   static constexpr int kTileBytes = G::kTileBytes;  // [128 x D] in fp16
   static constexpr int kSlots = 2;                  // K tiles and V tiles held each
-  static constexpr int kScaleSlots = 4;
+  static constexpr int kInfoSlots = 8;
   static constexpr int kAccO = 256;
-  static constexpr int kBarCount = 4 * kSlots + 11;
+  static constexpr int kBarCount = 4 * kSlots + 15;
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kSlots * kTileBytes;
-  static constexpr int kOffRs = kOffV + kSlots * kTileBytes;       // [2][256] row scales
-  static constexpr int kOffSc = kOffRs + 2 * kRows * 4;            // [kScaleSlots][8] float4
-  static constexpr int kOffBar = kOffSc + kScaleSlots * 8 * 16;
+  static constexpr int kOffRs = kOffV + kSlots * kTileBytes;       // [2][256] row exponents
+  static constexpr int kOffInfo = kOffRs + 2 * kRows;              // [kInfoSlots] TileInfo
+  static constexpr int kOffSeg = kOffInfo + kInfoSlots * 96;      // [kInfoSlots] SegInfo
+  static constexpr int kOffRaw = kOffSeg + kInfoSlots * 56;        // codes of one K, one V tile
+  static constexpr int kRawBytes = 128 * D;
+  static constexpr int kOffBar = kOffRaw + 2 * kRawBytes;
   static constexpr int kSmemBytes = 1024 + kOffBar + kBarCount * 8 + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
   static constexpr int kMinTiles = 4;  // least tiles of a CTA
   // registers a thread: 128 at launch (512 threads); 256 softmax threads, 128
-  // converters, 128 issuers
-  static constexpr int kSoftmaxRegs = 168, kConverterRegs = 112, kIssuerRegs = 64;
+  // converters, 128 issuers and producer
+  static constexpr int kSoftmaxRegs = 160, kConverterRegs = 96, kIssuerRegs = 96;
   static_assert(256 * kSoftmaxRegs + 128 * (kConverterRegs + kIssuerRegs) <= 512 * 128,
                 "register shares beyond the launch's total would wait forever");
 };
@@ -241,7 +364,7 @@ __global__ void __launch_bounds__(512, 1)
   constexpr int KPA = G::kAtomElems / 16;  // K steps of 16 in one swizzle atom
   constexpr int kRowChunks = D / 16;       // 16-byte code chunks of a key
   constexpr int kRowsPerPass = 128 / kRowChunks;
-  constexpr int kPasses = 128 / kRowsPerPass;  // 8 (d = 128) or 4 loads a thread and tile
+  constexpr int kPasses = 128 / kRowsPerPass;  // 8 (d = 128) or 4 chunks a thread and tile
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -250,8 +373,11 @@ __global__ void __launch_bounds__(512, 1)
   auto qbuf = [&](int h) { return sbase + h * C::kTileBytes; };
   auto kbuf = [&](int s) { return sbase + C::kOffK + s * C::kTileBytes; };
   auto vbuf = [&](int s) { return sbase + C::kOffV + s * C::kTileBytes; };
-  float* s_rs = reinterpret_cast<float*>(smem + C::kOffRs);
-  const uint32_t s_sc = sbase + C::kOffSc;
+  int8_t* s_rs = reinterpret_cast<int8_t*>(smem + C::kOffRs);
+  TileInfo* s_info = reinterpret_cast<TileInfo*>(smem + C::kOffInfo);
+  SegInfo* s_seg = reinterpret_cast<SegInfo*>(smem + C::kOffSeg);
+  constexpr uint32_t kRing = C::kInfoSlots - 1;
+  const uint32_t kraw = sbase + C::kOffRaw, vraw = kraw + C::kRawBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   const uint32_t bar0 = smem_u32(bars);
   constexpr int S = C::kSlots;
@@ -265,7 +391,10 @@ __global__ void __launch_bounds__(512, 1)
   auto pfull = [&](int h) { return bar0 + 8u * (4 * S + 4 + h); };  // P_h written, O_h scaled
   auto ofull = [&](int h) { return bar0 + 8u * (4 * S + 6 + h); };  // O_h of the segment done
   auto ofree = [&](int h) { return bar0 + 8u * (4 * S + 8 + h); };  // O_h read
-  const uint32_t done_bar = bar0 + 8u * (4 * S + 10);
+  // codes of a tile landed / read; t = 0: K, 1: V
+  auto rfull = [&](int t) { return bar0 + 8u * (4 * S + 10 + t); };
+  auto rempty = [&](int t) { return bar0 + 8u * (4 * S + 12 + t); };
+  const uint32_t done_bar = bar0 + 8u * (4 * S + 14);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBarCount);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -286,6 +415,8 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(pfull(h), 4);
       mbar_init(ofull(h), 1);
       mbar_init(ofree(h), 4);
+      mbar_init(rfull(h), 1);
+      mbar_init(rempty(h), 4);
     }
     mbar_init(done_bar, 2);
     *abort = 0;
@@ -303,11 +434,13 @@ __global__ void __launch_bounds__(512, 1)
   if (threadIdx.x == 0) p.desc[8 * blockIdx.x] = 0;   // nothing to join, unless set below
 
   const int used = fs.TQ * p.G;  // rows of a half in use
+  const uint32_t total = fs.n[blockIdx.x];  // tiles of this CTA
+  const int gm = (65536 + p.G - 1) / p.G;
   if (warp >= 12) {
-    // ------------------------------------------------------------ MMA issuers
     reg_dec<C::kIssuerRegs>();
     const int me = warp - 12;
     if (me < 2 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuers
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
       constexpr uint64_t kStep = C::kTileBytes >> 4;  // next buffer, in the address field
@@ -315,150 +448,165 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t kd = smem_desc(kbuf(0), 16, G::kGroupBytes, G::kLayout);
       const uint64_t vd = smem_desc(vbuf(0), G::kAtomTileBytes, G::kGroupBytes, G::kLayout);
       const uint32_t ts = tmem + me * 128, to = tmem + C::kAccO + me * D;
-      uint32_t n = 0, seg = 0;  // tiles and segments so far
-      FrameCursor cur;
-      cur.init(p, fs);
-      bool ok = true;
-      for (; cur.live && ok; cur.next(p, fs), ++seg) {
-        ok = mbar_wait(qfull, seg & 1u, abort, kCode);
-        auto issue_s = [&](uint32_t k) {  // S of tile k of this CTA
-          if (!mbar_wait(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
-          tc_fence_after();
-          const uint64_t b0 = kd + (k & 1u) * kStep;
+      uint32_t seg = 0;
+      auto issue_s = [&](uint32_t k) {  // S of tile k of this CTA
+        if (!mbar_wait_idle(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
+        const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&s_info[k & kRing].flags);
+        if ((flags & kTileFirst) && !mbar_wait_idle(qfull, seg & 1u, abort, kCode)) return false;
+        tc_fence_after();
+        const uint64_t b0 = kd + (k & 1u) * kStep;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off =
-                static_cast<uint64_t>(((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4);
-            mma_bf16(ts, qd + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(sfull(me));
-          mma_commit(kempty(k & 1u));
-          return true;
-        };
-        if (ok) ok = issue_s(n);
-        for (int t = cur.t0; t < cur.t1 && ok; ++t, ++n) {
-          const bool first = t == cur.t0, last = t + 1 == cur.t1;
-          if (last) mma_commit(qempty);  // every S of the segment has been issued
-          if (first && !mbar_wait(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ok = false;
-          if (!ok || !mbar_wait(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
-              !mbar_wait(pfull(me), n & 1u, abort, kCode)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t b0 = vd + (n & 1u) * kStep;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // 16 keys = 8 columns of P
-            mma_bf16_ts(to, ts + kk * 8, b0 + static_cast<uint64_t>((kk * 2 * G::kGroupBytes) >> 4),
-                        idesc_o, (first && kk == 0) ? 0u : 1u);
-          mma_commit(vempty(n & 1u));
-          if (last)
-            mma_commit(ofull(me));
-          else
-            ok = issue_s(n + 1);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off =
+              static_cast<uint64_t>(((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4);
+          mma_bf16(ts, qd + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
         }
+        mma_commit(sfull(me));
+        mma_commit(kempty(k & 1u));
+        if (flags & kTileLast) mma_commit(qempty);  // every S of the segment has been issued
+        return true;
+      };
+      bool ok = total > 0 && issue_s(0);
+      for (uint32_t n = 0; n < total && ok; ++n) {
+        const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&s_info[n & kRing].flags);
+        if (((flags & kTileFirst) && !mbar_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
+            !mbar_wait_idle(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
+            !mbar_wait_idle(pfull(me), n & 1u, abort, kCode))
+          break;
+        tc_fence_after();
+        const uint64_t b0 = vd + (n & 1u) * kStep;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)  // 16 keys = 8 columns of P
+          mma_bf16_ts(to, ts + kk * 8,
+                      b0 + static_cast<uint64_t>((kk * 2 * G::kGroupBytes) >> 4), idesc_o,
+                      ((flags & kTileFirst) && kk == 0) ? 0u : 1u);
+        mma_commit(vempty(n & 1u));
+        if (flags & kTileLast) {
+          mma_commit(ofull(me));
+          ++seg;
+        }
+        if (n + 1 < total) ok = issue_s(n + 1);
       }
       mma_commit(done_bar);
       mbar_wait_drain(done_bar, 0);
+    } else if (me == 2) {
+      // ------------------------------------------------------------- producer
+      const int P = 1 << p.p_shift;
+      const int64_t page_bytes = (static_cast<int64_t>(p.Hkv) << p.p_shift) * D;
+      const uint32_t chunk = static_cast<uint32_t>(D) << p.p_shift;  // one page of one head
+      const int copies = 128 >> p.p_shift, per = P >> 4;  // pages of a tile, groups of a page
+      uint32_t n = 0, seg = 0, issued[2] = {0, 0};
+      bool ok = true;
+      FrameCursor cur;
+      for (cur.init(p, fs); cur.live && ok; cur.next(p, fs), ++seg) {
+        const int* row = p.table + static_cast<int64_t>(cur.r) * p.max_pages;
+        for (int t = cur.t0; t < cur.t1 && ok; ++t, ++n) {
+          const int base = cur.v.pos(t, C::BK);
+          const int a = base + 16 * (lane & 7);  // lanes 8 .. repeat lanes 0 .. 7
+          const int j = a >> p.p_shift;
+          const bool vis = a < cur.v.hi && (a + 16 > cur.v.lo || a < cur.v.sink);
+          int pg = vis && j < p.max_pages ? row[j] : -1;
+          if (pg >= p.pages) pg = -1;
+          float ks = 0.f, vs = 0.f;
+          if (pg >= 0) {
+            const int64_t x = static_cast<int64_t>(pg) * p.Hkv + cur.h;
+            ks = p.ks[x];
+            vs = p.vs[x];
+          }
+          // positive floats order like their bits
+          float kt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ks)));
+          float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs)));
+          if (!(kt > 0.f)) kt = 1.f;
+          if (!(vt > 0.f)) vt = 1.f;
+          const uint32_t bad = __ballot_sync(0xffffffffu, vis && pg < 0) & 255u;
+          const uint32_t scale_k = __any_sync(0xffffffffu, pg >= 0 && ks != kt) ? kTileScaleK : 0u;
+          const uint32_t scale_v = __any_sync(0xffffffffu, pg >= 0 && vs != vt) ? kTileScaleV : 0u;
+          const bool all = base + C::BK <= cur.v.sink ||
+                           (base >= cur.v.lo && base + C::BK <= cur.v.hi);
+          // Safe to write: raw codes of tile n - 2 have been read, after the
+          // converters saw S of tile n - 4 complete; so every softmax warp is
+          // past tile n - 5 (and past the segments that ended there).
+          TileInfo& info = s_info[n & kRing];
+          if (t == cur.t0 && lane == 0) {
+            const int t_unit = cur.i * 2 * fs.TQ;
+            SegInfo& si = s_seg[seg & kRing];
+            si.row0 = (static_cast<long long>(cur.s.c0) + t_unit) * p.H + cur.h * p.G;
+            si.tokens = cur.s.n - t_unit;
+            si.p0 = cur.s.p0 + t_unit;
+            si.len = cur.s.len;
+            si.lo = cur.v.lo;
+            si.hi = cur.v.hi;
+            si.sink = cur.v.sink;
+            si.whole = cur.t0 == 0 && cur.t1 == cur.v.nb;
+            si.starts = cur.t0 == 0;
+            si.c0 = cur.s.c0;
+            si.unit_row = t_unit * p.G;
+            si.h = cur.h;
+            si.rest = cur.v.nb - cur.t1;
+          }
+          // one page's share of the tile, by lane
+          const int src_lane = (lane < copies ? lane : 0) * per;
+          const int cpg = __shfl_sync(0xffffffffu, pg, src_lane);
+          // a page whose first group is invisible may still show a later one
+          int use = cpg;
+#pragma unroll
+          for (int g = 1; g < 8; ++g) {
+            const int o = __shfl_sync(0xffffffffu, pg, (src_lane + g) & 7);
+            if (g < per && use < 0) use = o;
+          }
+          const bool mine = lane < copies && use >= 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * chunk;
+          if (lane < 8) {
+            const __half2 kf = __float2half2_rn(ks * (1.0f / kt)), vf = __float2half2_rn(vs * (1.0f / vt));
+            info.kfac[lane] = *reinterpret_cast<const uint32_t*>(&kf);
+            info.vfac[lane] = *reinterpret_cast<const uint32_t*>(&vf);
+            if (lane == 0) {
+              const float lv = lg2_approx(vt);
+              info.ks = kt;
+              info.lv = lv;
+              info.iv = ex2_approx(-lv);
+              info.flags = bad | (all ? kTileAll : 0u) | scale_k | scale_v |
+                           (t == cur.t0 ? kTileFirst : 0u) | (t + 1 == cur.t1 ? kTileLast : 0u);
+              info.base = base;
+            }
+          }
+          __syncwarp();
+          const int64_t off = (mine ? use : 0) * page_bytes + static_cast<int64_t>(cur.h) * chunk;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!warp_wait_idle(rempty(w), (n & 1u) ^ 1u, abort, kCode)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(rfull(w), bytes);
+            __syncwarp();
+            if (mine)
+              bulk_load((w ? vraw : kraw) + lane * chunk, (w ? p.v8 : p.k8) + off, chunk,
+                        rfull(w));
+            ++issued[w];
+          }
+        }
+      }
+      for (int w = 0; w < 2; ++w)  // copies in flight land before the CTA ends
+        if (issued[w] > 0) mbar_wait_drain(rfull(w), (issued[w] - 1) & 1u);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------- converters
     reg_dec<C::kConverterRegs>();
-    const int cw = warp - 8, ct = threadIdx.x - 256;
+    const int ct = threadIdx.x - 256;
     const int ch = ct % kRowChunks, row0 = ct / kRowChunks;
-    const int P = 1 << p.p_shift;
-    const int64_t page_rows = static_cast<int64_t>(p.Hkv) << p.p_shift;
-    uint4 ka[kPasses], va[kPasses];
-    float ksc = 1.f, vsc = 0.f;  // lanes 0 .. 7 of every warp: scales of 16-key group `lane`
-    FrameCursor ld;              // the tile loaded next
-    ld.init(p, fs);
-    int lt = ld.t0;
-    int page_of[8];              // pages of the tile's 16-key groups (-1: nothing visible there)
-    int64_t off[kPasses];        // byte offset of this thread's chunk in every pass (-1: zeros)
-    auto locate = [&]() {        // pages and offsets of tile lt of ld
-      const int base = ld.v.pos(lt, C::BK);
-      const int* row = p.table + static_cast<int64_t>(ld.r) * p.max_pages;
-      const int a = base + 16 * (lane & 7);
-      const int j = a >> p.p_shift;
-      int pg = -1;
-      if (j < p.max_pages && a < ld.v.hi && (a + 16 > ld.v.lo || a < ld.v.sink)) pg = row[j];
-      if (pg >= p.pages) pg = -1;
-      ksc = 1.f;
-      vsc = 0.f;
-      if (pg >= 0 && cw == 0 && lane < 8) {
-        const int64_t x = static_cast<int64_t>(pg) * p.Hkv + ld.h;
-        ksc = p.ks[x];
-        vsc = p.vs[x];
-      }
-#pragma unroll
-      for (int g = 0; g < 8; ++g) page_of[g] = __shfl_sync(0xffffffffu, pg, g);
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int kr = i * kRowsPerPass + row0;
-        const int key = base + kr;
-        int pgk = page_of[i * kRowsPerPass / 16];
-        if (kRowsPerPass > 16 && row0 >= 16) pgk = page_of[i * kRowsPerPass / 16 + 1];
-        off[i] = pgk >= 0 && ld.v.sees(key)
-                     ? (pgk * page_rows + (static_cast<int64_t>(ld.h) << p.p_shift) +
-                        (key & (P - 1))) * D + ch * 16
-                     : -1;
-      }
-    };
-    auto load = [&](uint4 (&x)[kPasses], const uint8_t* src) {
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (off[i] >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(src + off[i]));
-      }
-    };
-    auto advance = [&]() {
-      if (++lt >= ld.t1) {
-        ld.next(p, fs);
-        lt = ld.t0;
-      }
-    };
-    // 16 codes -> 32 bytes of fp16 in the swizzled row; the odd half of the
-    // lanes writes its two chunks in the other order (bank conflicts)
-    auto convert = [&](const uint4 (&x)[kPasses], uint32_t buf) {
-      const int c2 = (ch * 2) & 7;  // first 16-byte chunk within its 128-byte atom row
-      const uint32_t atom = static_cast<uint32_t>(ch * 2 / 8) * G::kAtomTileBytes;
-      const bool swap = (ch & 4) != 0;
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int kr = i * kRowsPerPass + row0;
-        const uint32_t rowp = buf + atom + kr * 128;
-        uint4 a, b;
-        a.x = e4m3x2_to_f16x2(x[i].x & 0xFFFFu);
-        a.y = e4m3x2_to_f16x2(x[i].x >> 16);
-        a.z = e4m3x2_to_f16x2(x[i].y & 0xFFFFu);
-        a.w = e4m3x2_to_f16x2(x[i].y >> 16);
-        b.x = e4m3x2_to_f16x2(x[i].z & 0xFFFFu);
-        b.y = e4m3x2_to_f16x2(x[i].z >> 16);
-        b.z = e4m3x2_to_f16x2(x[i].w & 0xFFFFu);
-        b.w = e4m3x2_to_f16x2(x[i].w >> 16);
-        const uint32_t pa = rowp + ((c2 ^ (kr & 7)) << 4);
-        const uint32_t pb = rowp + (((c2 + 1) ^ (kr & 7)) << 4);
-        st_shared_v4(swap ? pb : pa, swap ? b : a);
-        st_shared_v4(swap ? pa : pb, swap ? a : b);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    };
-    if (ld.live) {
-      locate();
-      load(ka, p.k8);
-      load(va, p.v8);
-    }
-    FrameCursor cur;
-    cur.init(p, fs);
-    uint32_t n = 0, seg = 0;
-    bool ok = true;
-    for (; cur.live && ok; cur.next(p, fs), ++seg) {
-      // ---- queries: bf16 -> fp16, scaled per row
+    const int c2 = (ch * 2) & 7;  // first 16-byte fp16 chunk within its 128-byte atom row
+    const uint32_t atom = static_cast<uint32_t>(ch * 2 / 8) * G::kAtomTileBytes;
+    const bool swap = (ch & 4) != 0;  // these lanes write their two chunks in the other order
+                                      // (bank conflicts)
+    // ---- queries of segment `seg`: bf16 -> fp16, scaled per row
+    auto convert_q = [&](uint32_t seg) {
       constexpr int kQChunks = D / 8, kQRows = 128 / kQChunks, kBatch = 8;
-      if (!warp_wait(qempty, (seg & 1u) ^ 1u, abort, kCode)) break;
+      if (!warp_wait_idle(qempty, (seg & 1u) ^ 1u, abort, kCode)) return false;
+      const SegInfo& si = s_seg[seg & kRing];
       const int qc = ct % kQChunks, qr0 = ct / kQChunks;
-      const int t_unit = cur.i * 2 * fs.TQ;
+      const __nv_bfloat16* qp = p.q + si.row0 * D + qc * 8;
+      const int tokens = si.tokens;
 #pragma unroll 1
       for (int pass = 0; pass < 256 / kQRows; pass += kBatch) {
         uint4 x[kBatch];
@@ -466,12 +614,12 @@ __global__ void __launch_bounds__(512, 1)
         for (int i = 0; i < kBatch; ++i) {
           const int row = (pass + i) * kQRows + qr0;
           const int lr = row & 127;
-          const int t = t_unit + (row >> 7) * fs.TQ + lr / p.G;
+          const int lt = small_div(lr, gm);
+          const int t = (row >> 7) * fs.TQ + lt;
           x[i] = make_uint4(0, 0, 0, 0);
-          if (lr < used && t < cur.s.n)
+          if (lr < used && t < tokens)
             x[i] = __ldg(reinterpret_cast<const uint4*>(
-                p.q + ((static_cast<int64_t>(cur.s.c0) + t) * p.H + cur.h * p.G + lr % p.G) * D +
-                qc * 8));
+                qp + (static_cast<int64_t>(t) * p.H + (lr - lt * p.G)) * D));
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -482,8 +630,8 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int o = kQChunks / 2; o > 0; o >>= 1)
             mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          float f, inv;
-          row_scale(mx, f, inv);
+          const int up = row_exponent(mx);
+          const float f = exp2_int(up);
           uint4 w;
           w.x = pack_f16x2(bf16lo_to_f32(x[i].x) * f, bf16hi_to_f32(x[i].x) * f);
           w.y = pack_f16x2(bf16lo_to_f32(x[i].y) * f, bf16hi_to_f32(x[i].y) * f);
@@ -493,45 +641,83 @@ __global__ void __launch_bounds__(512, 1)
           st_shared_v4(qbuf(row >> 7) + (qc >> 3) * G::kAtomTileBytes + lr * 128 +
                            (((qc & 7) ^ (lr & 7)) << 4),
                        w);
-          if (qc == 0) s_rs[(seg & 1u) * C::kRows + row] = inv * p.sl2;
+          if (qc == 0) s_rs[(seg & 1u) * C::kRows + row] = static_cast<int8_t>(up);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-      // ---- key / value tiles
-      for (int t = cur.t0; t < cur.t1; ++t, ++n) {
-        const int sl = n & 1u;
-        const uint32_t ph = ((n >> 1) & 1u) ^ 1u;
-        if (!warp_wait(kempty(sl), ph, abort, kCode)) {
+      return true;
+    };
+    uint32_t seg = 0;
+    bool ok = true;
+    for (uint32_t n = 0; n < total && ok; ++n) {
+      const int sl = n & 1u;
+      const TileInfo& info = s_info[n & kRing];
+#pragma unroll 1  // K, then V: one copy of the code
+      for (int w = 0; w < 2; ++w) {
+        if (!warp_wait_idle(rfull(w), n & 1u, abort, kCode)) {
           ok = false;
           break;
         }
-        convert(ka, kbuf(sl));
-        if (cw == 0 && lane < 8) {
-          // scale slot n % 4: its last reader finished tile n - 4 before S of
-          // tile n - 2 was issued, which the wait above has seen complete
-          const float lv = lg2_approx(vsc);  // -inf where nothing is visible
-          const float iv = vsc > 0.f ? ex2_approx(-lv) : 0.f;
-          st_shared_v4(s_sc + (n & 3u) * 128 + lane * 16,
-                       make_uint4(__float_as_uint(ksc), __float_as_uint(lv), __float_as_uint(iv),
-                                  0u));
+        const uint32_t flags = *const_cast<volatile const uint32_t*>(&info.flags);
+        if (w == 0 && (flags & kTileFirst) && !convert_q(seg)) {
+          ok = false;
+          break;
         }
+        uint4 x[kPasses];
+        const uint32_t raw = (w ? vraw : kraw) + ct * 16;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) x[i] = ld_shared_v4(raw + i * 2048);
+        if ((flags & (kTileBad | kTileAll)) != kTileAll) {
+          // uniform: keys that no row sees, or whose page is missing
+          const SegInfo& si = s_seg[seg & kRing];
+          const int key0 = info.base + row0, lo = si.lo, hi = si.hi, sink = si.sink;
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i)
+            if (!(key0 + i * kRowsPerPass < hi &&
+                  (key0 + i * kRowsPerPass >= lo || key0 + i * kRowsPerPass < sink)) ||
+                (flags >> (kRowsPerPass > 16 ? 2 * i + (row0 >> 4) : i) & 1))
+              x[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (!warp_wait_idle(w ? vempty(sl) : kempty(sl), ((n >> 1) & 1u) ^ 1u, abort, kCode)) {
+          ok = false;
+          break;
+        }
+        const uint32_t buf = (w ? vbuf(sl) : kbuf(sl)) + atom;
+        const bool scaled = flags & (w ? kTileScaleV : kTileScaleK);  // uniform
+        const uint32_t* fac = w ? info.vfac : info.kfac;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int kr = i * kRowsPerPass + row0;
+          uint32_t y[8];
+          const uint32_t c[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = e4m3x2_to_f16x2((e & 1) ? c[e >> 1] >> 16 : c[e >> 1] & 0xFFFFu);
+          if (scaled) {
+            const uint32_t fw = fac[kRowsPerPass > 16 ? 2 * i + (row0 >> 4) : i];
+            const __half2 f = *reinterpret_cast<const __half2*>(&fw);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&y[e]), f);
+              y[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          }
+          const uint32_t pa = buf + kr * 128 + ((c2 ^ (kr & 7)) << 4);
+          const uint32_t pb = buf + kr * 128 + (((c2 + 1) ^ (kr & 7)) << 4);
+          const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]);
+          const uint4 hi = make_uint4(y[4], y[5], y[6], y[7]);
+          st_shared_v4(swap ? pb : pa, swap ? hi : lo);
+          st_shared_v4(swap ? pa : pb, swap ? lo : hi);
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(kfull(sl));
-        advance();
-        const bool more = ld.live;
-        if (!warp_wait(vempty(sl), ph, abort, kCode)) {
-          ok = false;
-          break;
+        if (lane == 0) {
+          mbar_arrive(w ? vfull(sl) : kfull(sl));
+          mbar_arrive(rempty(w));  // every code has been used: no load of one is outstanding
         }
-        if (more) {
-          locate();
-          load(ka, p.k8);
-        }
-        convert(va, vbuf(sl));
-        if (lane == 0) mbar_arrive(vfull(sl));
-        if (more) load(va, p.v8);
+        if (w == 1 && (flags & kTileLast)) ++seg;
       }
     }
   } else {
@@ -539,183 +725,224 @@ __global__ void __launch_bounds__(512, 1)
     reg_inc<C::kSoftmaxRegs>();
     const int half = warp >> 2, q4 = warp & 3;
     const int row = q4 * 32 + lane;  // row of the half
+    const int row_t = small_div(row, gm), row_g = row - row_t * p.G;
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t ts = tmem + lane_base + half * 128;
     const uint32_t to = tmem + lane_base + C::kAccO + half * D;
-    uint32_t n = 0, seg = 0;
-    FrameCursor cur;
-    cur.init(p, fs);
-    for (; cur.live; cur.next(p, fs), ++seg) {
-      const int t = cur.i * 2 * fs.TQ + half * fs.TQ + row / p.G;
-      const bool have = row < used && t < cur.s.n;
-      // rows that hold no query see everything: they cost no mask
-      const int hi = have ? key_hi(p, cur.s, cur.s.p0 + t) : INT32_MAX;
-      const int lo = have ? key_lo(p, cur.s.p0 + t) : 0;
-      bool ok = true;
-      float rs = 0.f, m = -INFINITY, l = 0.f;
-      for (int tile = cur.t0; tile < cur.t1 && ok; ++tile, ++n) {
-        const int base = cur.v.pos(tile, C::BK);
-        if (!warp_wait_fast(sfull(half), n & 1u, abort, kCode)) {
-          ok = false;
-          break;
+    uint32_t seg = 0;
+    int hi = 0, lo = 0;
+    float rs = 0.f, m = -INFINITY, l = 0.f;
+    for (uint32_t n = 0; n < total; ++n) {
+      if (!warp_wait_idle(sfull(half), n & 1u, abort, kCode)) break;
+      tc_fence_after();
+      const float4 info = ld_shared_f4(smem_u32(&s_info[n & kRing].ks));
+      const int base = *const_cast<volatile int*>(&s_info[n & kRing].base);
+      const uint32_t flags = __float_as_uint(info.w);
+      {
+        if (flags & kTileFirst) {
+          const SegInfo& si = s_seg[seg & kRing];
+          const int t = half * fs.TQ + row_t;
+          const bool have = row < used && t < si.tokens;
+          CacheSeq s;
+          s.len = si.len;
+          // rows that hold no query see everything: they cost no mask
+          hi = have ? key_hi(p, s, si.p0 + t) : INT32_MAX;
+          lo = have ? key_lo(p, si.p0 + t) : 0;
+          // the row scales of segment seg are written before its first S and
+          // replaced after the last P of segment seg + 1
+          rs = exp2_int(-s_rs[(seg & 1u) * C::kRows + half * 128 + row]) * p.sl2;
+          m = -INFINITY;
+          l = 0.f;
         }
-        tc_fence_after();
-        // the row scales of segment seg are written before its first S and
-        // replaced after the last P of segment seg + 1
-        if (tile == cur.t0) rs = s_rs[(seg & 1u) * C::kRows + half * 128 + row];
-        uint32_t s[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32cols(ts + c * 32, s[c]);
-        tmem_wait_ld();
-        const bool whole = base >= lo && base + C::BK <= hi;
-        if (!__all_sync(0xffffffffu, whole)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int key = base + c * 32 + e;
-              if (!(key < hi && (key >= lo || key < p.n_sink)))
-                s[c][e] = __float_as_uint(-INFINITY);
-            }
-        }
-        const uint32_t sc = s_sc + (n & 3u) * 128;
-        float mt = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const uint32_t* x = &s[g >> 1][(g & 1) * 16];
-          float a = fmax3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-          float b = fmax3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
-          a = fmax3(a, __uint_as_float(x[6]), __uint_as_float(x[7]));
-          b = fmax3(b, __uint_as_float(x[8]), __uint_as_float(x[9]));
-          a = fmax3(a, __uint_as_float(x[10]), __uint_as_float(x[11]));
-          b = fmax3(b, __uint_as_float(x[12]), __uint_as_float(x[13]));
-          a = fmax3(a, __uint_as_float(x[14]), __uint_as_float(x[15]));
-          const float4 k = ld_shared_f4(sc + g * 16);
-          mt = fmaxf(mt, fmaf(fmaxf(a, b), rs * k.x, k.y));
-        }
-        const bool grow = mt > m + kCacheLazy;  // also the first visible key: m = -inf
-        if (__any_sync(0xffffffffu, grow && tile != cur.t0)) {
-          // O of the previous tiles is complete: S of this tile was issued
-          // after the last P V by the same thread
-          const float f = grow ? (m == -INFINITY ? 0.f : ex2_approx(m - mt)) : 1.0f;
-          if (grow) {
-            l *= f;
-            m = mt;
-          }
+        const uint32_t bad = flags & kTileBad;
+        const bool masked = !__all_sync(0xffffffffu, base >= lo && base + C::BK <= hi && bad == 0);
+        const float fg = rs * info.x;
+        const uint64_t f2 = f2_pack(fg, fg);
+        float tsum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld_16cols(to + c * 16, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_16cols(to + c * 16, o);
-          }
-          tmem_wait_st();
-        } else if (grow) {
-          m = mt;
-        }
-        const float sh = m == -INFINITY ? 0.f : kCacheBias - m;
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
+        for (int hb = 0; hb < 2; ++hb) {  // 64 keys at a time: their P' stays in 32 registers
+          bool need = __any_sync(0xffffffffu, m == -INFINITY);  // take the maximum first
           uint32_t pw[32];
+          float hsum;
+          for (;;) {
+            if (need) {
+              float mt = -INFINITY;
+#pragma unroll 1
+              for (int c = 2 * hb; c < 2 * hb + 2; ++c) {
+                uint32_t s[32];
+                tmem_ld_32cols(ts + c * 32, s);
+                tmem_wait_ld_of(s);
+                if (masked)
+                  hide(s, visible_bits(base + c * 32, lo, hi, p.n_sink, bad >> (2 * c)));
+                float mx[4] = {mt, mt, mt, mt};
 #pragma unroll
-          for (int gg = 0; gg < 4; ++gg) {
-            const int g = hb * 4 + gg;
-            const float4 k = ld_shared_f4(sc + g * 16);
-            const float fg = rs * k.x, sg = k.y + sh;
-            const uint64_t f2 = f2_pack(fg, fg), s2 = f2_pack(sg, sg);
-            uint64_t sum = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t* x = &s[g >> 1][(g & 1) * 16 + 2 * e];
-              float a0, a1, y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), f2, s2), a0,
-                        a1);
-              if ((e & 3) == 0) {
-                exp2_poly3_x2(a0, a1, y0, y1);
-              } else {
-                y0 = ex2_approx(a0);
-                y1 = ex2_approx(a1);
+                for (int e = 0; e < 32; e += 2)
+                  mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(s[e]),
+                                           __uint_as_float(s[e + 1]));
+                mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               }
-              sum = f2_add(sum, f2_pack(y0, y1));
-              pw[gg * 8 + e] = pack_f16x2(y0, y1);
+              const float x = fmaf(mt, fg, info.y);
+              // whole steps: the factor is a power of two, exact for P' and O
+              const float mn = m == -INFINITY ? x : m + ceilf(fmaxf(x - m, 0.f));
+              const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+              l *= f;
+              tsum *= f;
+              m = mn;
+              if (hb == 1) {  // the P' of the tile's first 64 keys is written already
+                uint32_t o[32];
+                tmem_wait_st();
+                tmem_ld_32cols(ts, o);
+                tmem_wait_ld_of(o);
+                const __half2 f16 = __float2half2_rn(f);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f16);
+                  o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                tmem_st_32cols(ts, o);
+                tmem_wait_st();
+              }
+              if (!(flags & kTileFirst)) {
+                // O of the previous tiles is complete: S of this tile was issued
+                // after the last P V by the same thread
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t o[32];
+                  tmem_ld_32cols(to + c * 32, o);
+                  tmem_wait_ld_of(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st_32cols(to + c * 32, o);
+                }
+                tmem_wait_st();
+              }
+            }
+            const float sg = m == -INFINITY ? 0.f : info.y + (kCacheBias - m);
+            const uint64_t s2 = f2_pack(sg, sg);
+            uint64_t sum[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = f2_pack(0.f, 0.f);
+            uint32_t s[2][32];  // 32 keys in work, the next 32 on their way
+            tmem_ld_32cols(ts + hb * 64, s[0]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_wait_ld_of(s[c]);
+              if (c == 0) tmem_ld_32cols(ts + hb * 64 + 32, s[1]);
+              uint32_t(&x)[32] = s[c];
+              if (masked)
+                hide(x, visible_bits(base + hb * 64 + c * 32, lo, hi, p.n_sink,
+                                     bad >> (4 * hb + 2 * c)));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float a0, a1, y0, y1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                 f2, s2),
+                          a0, a1);
+                if ((e & 3) == 0) {
+                  exp2_poly3_x2(a0, a1, y0, y1);
+                } else {
+                  y0 = ex2_approx(a0);
+                  y1 = ex2_approx(a1);
+                }
+                sum[e & 3] = f2_add(sum[e & 3], f2_pack(y0, y1));
+                pw[c * 16 + e] = pack_f16x2(y0, y1);
+              }
             }
             float l0, l1;
-            f2_unpack(sum, l0, l1);
-            l = fmaf(l0 + l1, k.z, l);
+            f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), l0, l1);
+            hsum = l0 + l1;
+            // every P' is at most the sum: below 2^15 all of them are fp16 numbers
+            if (need || __all_sync(0xffffffffu, hsum < 32768.0f)) break;
+            need = true;  // once: then P' is at most 2^kCacheBias
           }
           tmem_st_32cols(ts + hb * 32, pw);
+          tsum += hsum;
         }
+        l = fmaf(tsum, info.z, l);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(half));
       }
-      if (!ok || !warp_wait(ofull(half), seg & 1u, abort, kCode)) break;
-      tc_fence_after();
+      if (!(flags & kTileLast)) continue;
       // ---- the segment's result: out, or a partial when the unit goes on elsewhere
-      const bool starts = cur.t0 == 0, ends = cur.t1 == cur.v.nb;
-      const int64_t at = have ? ((static_cast<int64_t>(cur.s.c0) + t) * p.H + cur.h * p.G +
-                                 row % p.G) * D
-                              : 0;
+      const SegInfo& si = s_seg[seg & kRing];
+      const int t = half * fs.TQ + row_t;
+      const bool have = row < used && t < si.tokens;
+      const bool whole = si.whole;
+      const int64_t at = have ? (si.row0 + static_cast<int64_t>(t) * p.H + row_g) * D : 0;
+      const bool gate = have && whole && p.z != nullptr;
+      const uint4* zp = reinterpret_cast<const uint4*>(p.z + at);
+      if (!warp_wait_idle(ofull(half), seg & 1u, abort, kCode)) break;
+      tc_fence_after();
       const float rl = m == -INFINITY ? 0.f : 1.0f / l;
-      float* part = p.part + (2ll * blockIdx.x + (starts ? 1 : 0)) * C::kPartFloats;
+      float* part = p.part + (2ll * blockIdx.x + (si.starts ? 1 : 0)) * C::kPartFloats;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
+        uint4 zw[4];
+        if (gate) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) zw[q] = __ldg(zp + c * 4 + q);
+        }
         uint32_t o[32];
         tmem_ld_32cols(to + c * 32, o);
-        tmem_wait_ld();
-        if (!have) continue;
-        if (starts && ends) {
-          const uint4* zp = reinterpret_cast<const uint4*>(p.z + at + c * 32);
-          uint4* op = reinterpret_cast<uint4*>(p.out + at + c * 32);
+        tmem_wait_ld_of(o);
+        if (whole) {
+          uint32_t w[2][8];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float x0 = __uint_as_float(o[2 * q]) * rl, x1 = __uint_as_float(o[2 * q + 1]) * rl;
+            if (gate) {
+              const uint32_t zz = (&zw[q / 4].x)[q & 3];
+              x0 *= 1.0f / (1.0f + __expf(-bf16lo_to_f32(zz)));
+              x1 *= 1.0f / (1.0f + __expf(-bf16hi_to_f32(zz)));
+            }
+            w[q >> 3][q & 7] = pack_bf16x2(x0, x1);
+          }
+          if (have) {  // rows are 16-byte aligned, not always 32
+            uint4* op = reinterpret_cast<uint4*>(p.out + at + c * 32);
+            if ((reinterpret_cast<uintptr_t>(op) & 31) == 0) {
+              st_global_v8(op, w[0]);
+              st_global_v8(op + 2, w[1]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                op[q] = make_uint4(w[q >> 1][(q & 1) * 4], w[q >> 1][(q & 1) * 4 + 1],
+                                   w[q >> 1][(q & 1) * 4 + 2], w[q >> 1][(q & 1) * 4 + 3]);
+            }
+          }
+        } else if (have) {
+          // (rows that saw no key in this part hold zeros)
+          float* dst = part + (half * 128 + row) * D + c * 32;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[q * 8 + e]) * rl;
-            if (p.z != nullptr) {
-              const uint4 zw = __ldg(zp + q);
-              const uint32_t zz[4] = {zw.x, zw.y, zw.z, zw.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float zf = (e & 1) ? bf16hi_to_f32(zz[e >> 1]) : bf16lo_to_f32(zz[e >> 1]);
-                x[e] *= 1.0f / (1.0f + __expf(-zf));
-              }
-            }
-            op[q] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            const uint32_t v[8] = {o[8 * q],     o[8 * q + 1], o[8 * q + 2], o[8 * q + 3],
+                                   o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
+            st_global_v8(dst + q * 8, v);
           }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(part + (half * 128 + row) * D + c * 32);
-          // rows that saw no key in this part hold zeros in O already
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                 __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
         }
       }
-      if (!(starts && ends))
-        *reinterpret_cast<float2*>(part + C::kRows * D + 2 * (half * 128 + row)) =
-            make_float2(m, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree(half));
-      if (threadIdx.x == 0 && starts && !ends) {
+      if (!whole)
+        *reinterpret_cast<float2*>(part + C::kRows * D + 2 * (half * 128 + row)) =
+            make_float2(m, l);
+      if (threadIdx.x == 0 && si.starts && !whole) {
         // this unit's parts: this CTA, then every one up to the last tile
-        int parts = 1, rest = cur.v.nb - cur.t1;
+        int parts = 1, rest = si.rest;
         for (int c = blockIdx.x + 1; rest > 0 && c < static_cast<int>(gridDim.x); ++c) {
           ++parts;
           rest -= fs.n[c];
         }
         int* desc = p.desc + 8 * blockIdx.x;
-        desc[1] = cur.s.c0;
-        desc[2] = cur.i * 2 * fs.TQ * p.G;
-        desc[3] = cur.h;
-        desc[4] = min(2 * fs.TQ, cur.s.n - cur.i * 2 * fs.TQ) * p.G;
+        desc[1] = si.c0;
+        desc[2] = si.unit_row;
+        desc[3] = si.h;
+        desc[4] = min(2 * fs.TQ, si.tokens) * p.G;
         desc[0] = parts;
       }
+      ++seg;
     }
   }
 

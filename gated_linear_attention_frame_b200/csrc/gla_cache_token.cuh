@@ -120,14 +120,12 @@ __device__ __forceinline__ int64_t share_lo(int64_t total, int ctas, int c) {
   return total / ctas * c + total % ctas * c / ctas;
 }
 
-// 2^(14 - E) for a row whose largest magnitude has bf16 exponent E (zero and
-// non-finite rows: 1), as the factor and its inverse.
-__device__ __forceinline__ void row_scale(uint32_t amax_bits, float& f, float& inv) {
+// A query row is multiplied by 2^row_exponent before it becomes fp16: 14 - E for
+// a largest magnitude of bf16 exponent E (0 for zero and non-finite rows).
+__device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
   const int e = static_cast<int>(amax_bits >> 7);
   const int up = (e == 0 || e == 255) ? 0 : 14 - (e - 127);  // in [-113, 140]
-  const int c = up > 126 ? 126 : up;
-  f = exp2_int(c);
-  inv = exp2_int(-c);
+  return up > 126 ? 126 : up;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -389,9 +387,9 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       mx = max(mx & 0xFFFFu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      float f, inv;
-      row_scale(mx, f, inv);
-      rs[e] = inv * p.sl2;
+      const int up = row_exponent(mx);
+      const float f = exp2_int(up);
+      rs[e] = exp2_int(-up) * p.sl2;
 #pragma unroll
       for (int i = 0; i < KI; ++i)
 #pragma unroll
