@@ -25,7 +25,8 @@
 //   O_h += P_h V    A = P_h in TMEM (fp16, over the columns of S_h),
 //                   B = V tile [128 keys x d] MN-major
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).  One issuing
-// warp per half: P V of tile j, then S of tile j + 1 into the same columns (the tensor core runs one thread's
+// warp per half: P V of tile j (in two steps of 64 keys, as P is written), then
+// S of tile j + 1 into the same columns (the tensor core runs one thread's
 // products in order), while the other half's softmax runs; so the two halves
 // alternate between the tensor core and the exponentials.
 // Softmax: one thread per row.  P' = 2^(S f + lv - m + kCacheBias), f = key scale
@@ -33,8 +34,8 @@
 // of the row sum again).  The maximum of a tile is not taken as a rule: the
 // row's reference m stays while the sum of P' over 64 keys stays below 2^15
 // (then no P' leaves the fp16 range); otherwise, and on the first keys that a
-// row sees, they are read again, m becomes their maximum, and O is rescaled.  One pair of exponentials in four runs on the FMA pipe
-// (exp2_poly3_x2).
+// row sees, they are read again, m becomes their maximum, and O is rescaled.
+// One pair of exponentials in four runs on the FMA pipe (exp2_poly3_x2).
 // Warp roles: 0-3 / 4-7 softmax and epilogue of half 0 / 1, 8-11 converters,
 // 12 / 13 MMA issuers of half 0 / 1, 14 producer (15 idle: it completes the
 // register group).
@@ -117,6 +118,15 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // i / G for 0 <= i < 256 and 1 <= G <= 128, with m = (65536 + G - 1) / G (checked
 // for every i and G).
 __device__ __forceinline__ int small_div(int i, int m) { return (i * m) >> 16; }
@@ -133,18 +143,9 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// Which of the 32 keys from `key` on a row sees: [lo, hi) and the sinks, without
-// the 16-key groups of bad (two bits).
-__device__ __forceinline__ uint32_t visible_bits(int key, int lo, int hi, int n_sink,
-                                                 uint32_t bad) {
-  const uint32_t w = bits_below(hi - key) & (~bits_below(lo - key) | bits_below(n_sink - key));
-  return w & ~((bad & 1u ? 0xFFFFu : 0u) | (bad & 2u ? 0xFFFF0000u : 0u));
-}
-
-__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t visible) {
-#pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (!(visible >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
+// Which of the 16 keys from `key` on a row sees: [lo, hi) and the sinks.
+__device__ __forceinline__ uint32_t visible_bits(int key, int lo, int hi, int n_sink) {
+  return bits_below(hi - key) & (~bits_below(lo - key) | bits_below(n_sink - key));
 }
 
 // What the producer leaves about a tile and about a segment (a CTA's tiles of
@@ -188,7 +189,7 @@ struct FrameCfg {
   static constexpr int kSlots = 2;                  // K tiles and V tiles held each
   static constexpr int kInfoSlots = 8;
   static constexpr int kAccO = 256;
-  static constexpr int kBarCount = 4 * kSlots + 15;
+  static constexpr int kBarCount = 4 * kSlots + 19;
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kSlots * kTileBytes;
   static constexpr int kOffRs = kOffV + kSlots * kTileBytes;       // [2][256] row exponents
@@ -203,7 +204,7 @@ struct FrameCfg {
   static constexpr int kMinTiles = 4;  // least tiles of a CTA
   // registers a thread: 128 at launch (512 threads); 256 softmax threads, 128
   // converters, 128 issuers and producer
-  static constexpr int kSoftmaxRegs = 160, kConverterRegs = 96, kIssuerRegs = 96;
+  static constexpr int kSoftmaxRegs = 168, kConverterRegs = 88, kIssuerRegs = 88;
   static_assert(256 * kSoftmaxRegs + 128 * (kConverterRegs + kIssuerRegs) <= 512 * 128,
                 "register shares beyond the launch's total would wait forever");
 };
@@ -388,7 +389,9 @@ __global__ void __launch_bounds__(512, 1)
   const uint32_t qfull = bar0 + 8u * (4 * S);
   const uint32_t qempty = bar0 + 8u * (4 * S + 1);
   auto sfull = [&](int h) { return bar0 + 8u * (4 * S + 2 + h); };  // S_h landed
-  auto pfull = [&](int h) { return bar0 + 8u * (4 * S + 4 + h); };  // P_h written, O_h scaled
+  // the first (second) 64 keys of P_h are written; P V of the first 64 is done
+  auto pfull = [&](int h, int part) { return bar0 + 8u * (4 * S + (part ? 15 : 4) + h); };
+  auto pvdone = [&](int h) { return bar0 + 8u * (4 * S + 17 + h); };
   auto ofull = [&](int h) { return bar0 + 8u * (4 * S + 6 + h); };  // O_h of the segment done
   auto ofree = [&](int h) { return bar0 + 8u * (4 * S + 8 + h); };  // O_h read
   // codes of a tile landed / read; t = 0: K, 1: V
@@ -412,7 +415,9 @@ __global__ void __launch_bounds__(512, 1)
     mbar_init(qempty, 2);
     for (int h = 0; h < 2; ++h) {
       mbar_init(sfull(h), 1);
-      mbar_init(pfull(h), 4);
+      mbar_init(pfull(h, 0), 4);
+      mbar_init(pfull(h, 1), 4);
+      mbar_init(pvdone(h), 1);
       mbar_init(ofull(h), 1);
       mbar_init(ofree(h), 4);
       mbar_init(rfull(h), 1);
@@ -456,10 +461,9 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_after();
         const uint64_t b0 = kd + (k & 1u) * kStep;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off =
-              static_cast<uint64_t>(((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4);
-          mma_bf16(ts, qd + off, b0 + off, idesc_s, kk > 0 ? 1u : 0u);
+        for (uint32_t kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = ((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4;
+          mma_bf16(ts, qd + off, b0 + off, idesc_s, kk);
         }
         mma_commit(sfull(me));
         mma_commit(kempty(k & 1u));
@@ -471,15 +475,20 @@ __global__ void __launch_bounds__(512, 1)
         const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&s_info[n & kRing].flags);
         if (((flags & kTileFirst) && !mbar_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
             !mbar_wait_idle(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
-            !mbar_wait_idle(pfull(me), n & 1u, abort, kCode))
+            !mbar_wait_idle(pfull(me, 0), n & 1u, abort, kCode))
           break;
         tc_fence_after();
         const uint64_t b0 = vd + (n & 1u) * kStep;
+        const uint32_t keep = (flags & kTileFirst) ? 0u : 1u;  // add to O, or begin it
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // 16 keys = 8 columns of P
-          mma_bf16_ts(to, ts + kk * 8,
-                      b0 + static_cast<uint64_t>((kk * 2 * G::kGroupBytes) >> 4), idesc_o,
-                      ((flags & kTileFirst) && kk == 0) ? 0u : 1u);
+        for (uint32_t kk = 0; kk < 4; ++kk)  // 16 keys = 8 columns of P
+          mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, kk | keep);
+        mma_commit(pvdone(me));
+        if (!mbar_wait_idle(pfull(me, 1), n & 1u, abort, kCode)) break;
+        tc_fence_after();
+#pragma unroll
+        for (uint32_t kk = 4; kk < 8; ++kk)
+          mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, 1u);
         mma_commit(vempty(n & 1u));
         if (flags & kTileLast) {
           mma_commit(ofull(me));
@@ -495,7 +504,7 @@ __global__ void __launch_bounds__(512, 1)
       const int64_t page_bytes = (static_cast<int64_t>(p.Hkv) << p.p_shift) * D;
       const uint32_t chunk = static_cast<uint32_t>(D) << p.p_shift;  // one page of one head
       const int copies = 128 >> p.p_shift, per = P >> 4;  // pages of a tile, groups of a page
-      uint32_t n = 0, seg = 0, issued[2] = {0, 0};
+      uint32_t n = 0, seg = 0, issued = 0;  // copies of K and V tiles begun
       bool ok = true;
       FrameCursor cur;
       for (cur.init(p, fs); cur.live && ok; cur.next(p, fs), ++seg) {
@@ -544,17 +553,11 @@ __global__ void __launch_bounds__(512, 1)
             si.h = cur.h;
             si.rest = cur.v.nb - cur.t1;
           }
-          // one page's share of the tile, by lane
-          const int src_lane = (lane < copies ? lane : 0) * per;
-          const int cpg = __shfl_sync(0xffffffffu, pg, src_lane);
-          // a page whose first group is invisible may still show a later one
-          int use = cpg;
-#pragma unroll
-          for (int g = 1; g < 8; ++g) {
-            const int o = __shfl_sync(0xffffffffu, pg, (src_lane + g) & 7);
-            if (g < per && use < 0) use = o;
-          }
-          const bool mine = lane < copies && use >= 0;
+          // one page's share of the tile, by lane: the page of its first visible group
+          const uint32_t groups =
+              __ballot_sync(0xffffffffu, pg >= 0) & 255u & (((1u << per) - 1u) << (lane * per & 31));
+          const int use = __shfl_sync(0xffffffffu, pg, groups ? __ffs(groups) - 1 : 0);
+          const bool mine = lane < copies && groups != 0;
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * chunk;
           if (lane < 8) {
             const __half2 kf = __float2half2_rn(ks * (1.0f / kt)), vf = __float2half2_rn(vs * (1.0f / vt));
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           __syncwarp();
           const int64_t off = (mine ? use : 0) * page_bytes + static_cast<int64_t>(cur.h) * chunk;
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < 2; ++w) {
             if (!warp_wait_idle(rempty(w), (n & 1u) ^ 1u, abort, kCode)) {
               ok = false;
@@ -580,15 +583,16 @@ __global__ void __launch_bounds__(512, 1)
             }
             if (lane == 0) mbar_arrive_expect_tx(rfull(w), bytes);
             __syncwarp();
+            ++issued;
             if (mine)
               bulk_load((w ? vraw : kraw) + lane * chunk, (w ? p.v8 : p.k8) + off, chunk,
                         rfull(w));
-            ++issued[w];
           }
         }
       }
-      for (int w = 0; w < 2; ++w)  // copies in flight land before the CTA ends
-        if (issued[w] > 0) mbar_wait_drain(rfull(w), (issued[w] - 1) & 1u);
+      // copies in flight land before the CTA ends
+      if (issued > 0) mbar_wait_drain(rfull(0), ((issued + 1) / 2 - 1) & 1u);
+      if (issued > 1) mbar_wait_drain(rfull(1), (issued / 2 - 1) & 1u);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------- converters
@@ -599,50 +603,50 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t atom = static_cast<uint32_t>(ch * 2 / 8) * G::kAtomTileBytes;
     const bool swap = (ch & 4) != 0;  // these lanes write their two chunks in the other order
                                       // (bank conflicts)
-    // ---- queries of segment `seg`: bf16 -> fp16, scaled per row
+    // ---- queries of segment `seg`: all rows are copied to their places as bf16
+    // at once, then each thread turns its own chunks into fp16 in place, scaled
+    // per row
     auto convert_q = [&](uint32_t seg) {
-      constexpr int kQChunks = D / 8, kQRows = 128 / kQChunks, kBatch = 8;
+      constexpr int kQChunks = D / 8, kQRows = 128 / kQChunks;
       if (!warp_wait_idle(qempty, (seg & 1u) ^ 1u, abort, kCode)) return false;
       const SegInfo& si = s_seg[seg & kRing];
       const int qc = ct % kQChunks, qr0 = ct / kQChunks;
       const __nv_bfloat16* qp = p.q + si.row0 * D + qc * 8;
       const int tokens = si.tokens;
+      auto place = [&](int row) {
+        const int lr = row & 127;
+        return qbuf(row >> 7) + (qc >> 3) * G::kAtomTileBytes + lr * 128 +
+               (((qc & 7) ^ (lr & 7)) << 4);
+      };
 #pragma unroll 1
-      for (int pass = 0; pass < 256 / kQRows; pass += kBatch) {
-        uint4 x[kBatch];
+      for (int row = qr0; row < 256; row += kQRows) {
+        const int lr = row & 127;
+        const int lt = small_div(lr, gm);
+        const int t = (row >> 7) * fs.TQ + lt;
+        const bool have = lr < used && t < tokens;
+        cp_async16(place(row),
+                   qp + (have ? (static_cast<int64_t>(t) * p.H + (lr - lt * p.G)) * D : 0), have);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+#pragma unroll 2
+      for (int row = qr0; row < 256; row += kQRows) {
+        const uint4 x = ld_shared_v4(place(row));
+        uint32_t mx = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                               __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+        mx = max(mx & 0xFFFFu, mx >> 16);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = (pass + i) * kQRows + qr0;
-          const int lr = row & 127;
-          const int lt = small_div(lr, gm);
-          const int t = (row >> 7) * fs.TQ + lt;
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (lr < used && t < tokens)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(
-                qp + (static_cast<int64_t>(t) * p.H + (lr - lt * p.G)) * D));
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = (pass + i) * kQRows + qr0;
-          uint32_t mx = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                                 __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
-          mx = max(mx & 0xFFFFu, mx >> 16);
-#pragma unroll
-          for (int o = kQChunks / 2; o > 0; o >>= 1)
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int up = row_exponent(mx);
-          const float f = exp2_int(up);
-          uint4 w;
-          w.x = pack_f16x2(bf16lo_to_f32(x[i].x) * f, bf16hi_to_f32(x[i].x) * f);
-          w.y = pack_f16x2(bf16lo_to_f32(x[i].y) * f, bf16hi_to_f32(x[i].y) * f);
-          w.z = pack_f16x2(bf16lo_to_f32(x[i].z) * f, bf16hi_to_f32(x[i].z) * f);
-          w.w = pack_f16x2(bf16lo_to_f32(x[i].w) * f, bf16hi_to_f32(x[i].w) * f);
-          const int lr = row & 127;
-          st_shared_v4(qbuf(row >> 7) + (qc >> 3) * G::kAtomTileBytes + lr * 128 +
-                           (((qc & 7) ^ (lr & 7)) << 4),
-                       w);
-          if (qc == 0) s_rs[(seg & 1u) * C::kRows + row] = static_cast<int8_t>(up);
-        }
+        for (int o = kQChunks / 2; o > 0; o >>= 1)
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int up = row_exponent(mx);
+        const float f = exp2_int(up);
+        uint4 w;
+        w.x = pack_f16x2(bf16lo_to_f32(x.x) * f, bf16hi_to_f32(x.x) * f);
+        w.y = pack_f16x2(bf16lo_to_f32(x.y) * f, bf16hi_to_f32(x.y) * f);
+        w.z = pack_f16x2(bf16lo_to_f32(x.z) * f, bf16hi_to_f32(x.z) * f);
+        w.w = pack_f16x2(bf16lo_to_f32(x.w) * f, bf16hi_to_f32(x.w) * f);
+        st_shared_v4(place(row), w);
+        if (qc == 0) s_rs[(seg & 1u) * C::kRows + row] = static_cast<int8_t>(up);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -735,6 +739,8 @@ __global__ void __launch_bounds__(512, 1)
     for (uint32_t n = 0; n < total; ++n) {
       if (!warp_wait_idle(sfull(half), n & 1u, abort, kCode)) break;
       tc_fence_after();
+      uint32_t s[2][32];  // 32 keys in work, the next 32 on their way
+      tmem_ld_32cols(ts, s[0]);
       const float4 info = ld_shared_f4(smem_u32(&s_info[n & kRing].ks));
       const int base = *const_cast<volatile int*>(&s_info[n & kRing].base);
       const uint32_t flags = __float_as_uint(info.w);
@@ -755,10 +761,29 @@ __global__ void __launch_bounds__(512, 1)
           l = 0.f;
         }
         const uint32_t bad = flags & kTileBad;
-        const bool masked = !__all_sync(0xffffffffu, base >= lo && base + C::BK <= hi && bad == 0);
+        if (!__all_sync(0xffffffffu, base >= lo && base + C::BK <= hi && bad == 0)) {
+          // hidden keys: S = -inf, written back, in a pass of its own (few tiles
+          // need it, and inside the loops below its code would be fetched with
+          // theirs)
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            uint32_t x[16];
+            tmem_ld_16cols(ts + g * 16, x);
+            tmem_wait_ld_of(x);
+            uint32_t w = visible_bits(base + g * 16, lo, hi, p.n_sink);
+            if (bad >> g & 1u) w = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = (w >> e & 1u) ? x[e] : __float_as_uint(-INFINITY);
+            tmem_st_16cols(ts + g * 16, x);
+          }
+          tmem_wait_st();
+          tmem_ld_32cols(ts, s[0]);
+        }
         const float fg = rs * info.x;
         const uint64_t f2 = f2_pack(fg, fg);
         float tsum = 0.f;
+        bool gave_up = false;
 #pragma unroll 1
         for (int hb = 0; hb < 2; ++hb) {  // 64 keys at a time: their P' stays in 32 registers
           bool need = __any_sync(0xffffffffu, m == -INFINITY);  // take the maximum first
@@ -766,72 +791,61 @@ __global__ void __launch_bounds__(512, 1)
           float hsum;
           for (;;) {
             if (need) {
+              tmem_wait_ld_of(s[0]);  // the load on its way is taken again below
               float mt = -INFINITY;
 #pragma unroll 1
               for (int c = 2 * hb; c < 2 * hb + 2; ++c) {
-                uint32_t s[32];
-                tmem_ld_32cols(ts + c * 32, s);
-                tmem_wait_ld_of(s);
-                if (masked)
-                  hide(s, visible_bits(base + c * 32, lo, hi, p.n_sink, bad >> (2 * c)));
+                tmem_ld_32cols(ts + c * 32, s[0]);
+                tmem_wait_ld_of(s[0]);
                 float mx[4] = {mt, mt, mt, mt};
 #pragma unroll
                 for (int e = 0; e < 32; e += 2)
-                  mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(s[e]),
-                                           __uint_as_float(s[e + 1]));
+                  mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(s[0][e]),
+                                           __uint_as_float(s[0][e + 1]));
                 mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               }
               const float x = fmaf(mt, fg, info.y);
-              // whole steps: the factor is a power of two, exact for P' and O
+              // whole steps: the factor is a power of two, exact for O
               const float mn = m == -INFINITY ? x : m + ceilf(fmaxf(x - m, 0.f));
               const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
               l *= f;
               tsum *= f;
               m = mn;
-              if (hb == 1) {  // the P' of the tile's first 64 keys is written already
-                uint32_t o[32];
-                tmem_wait_st();
-                tmem_ld_32cols(ts, o);
-                tmem_wait_ld_of(o);
-                const __half2 f16 = __float2half2_rn(f);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f16);
-                  o[e] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                tmem_st_32cols(ts, o);
-                tmem_wait_st();
+              // O of the previous tiles is complete: S of this tile was issued
+              // after the last P V by the same thread; the first 64 keys of
+              // this tile may be in work still
+              if (hb == 1 && !warp_wait_idle(pvdone(half), n & 1u, abort, kCode)) {
+                gave_up = true;
+                break;
               }
-              if (!(flags & kTileFirst)) {
-                // O of the previous tiles is complete: S of this tile was issued
-                // after the last P V by the same thread
+              if (hb == 1 || !(flags & kTileFirst)) {
+                tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
-                  uint32_t o[32];
-                  tmem_ld_32cols(to + c * 32, o);
-                  tmem_wait_ld_of(o);
+                  tmem_ld_32cols(to + c * 32, s[0]);
+                  tmem_wait_ld_of(s[0]);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st_32cols(to + c * 32, o);
+                  for (int e = 0; e < 32; ++e)
+                    s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * f);
+                  tmem_st_32cols(to + c * 32, s[0]);
                 }
                 tmem_wait_st();
               }
+              tmem_ld_32cols(ts + hb * 64, s[0]);
             }
             const float sg = m == -INFINITY ? 0.f : info.y + (kCacheBias - m);
             const uint64_t s2 = f2_pack(sg, sg);
             uint64_t sum[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] = f2_pack(0.f, 0.f);
-            uint32_t s[2][32];  // 32 keys in work, the next 32 on their way
-            tmem_ld_32cols(ts + hb * 64, s[0]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               tmem_wait_ld_of(s[c]);
-              if (c == 0) tmem_ld_32cols(ts + hb * 64 + 32, s[1]);
+              if (c == 0)
+                tmem_ld_32cols(ts + hb * 64 + 32, s[1]);
+              else if (hb == 0)
+                tmem_ld_32cols(ts + 64, s[0]);
               uint32_t(&x)[32] = s[c];
-              if (masked)
-                hide(x, visible_bits(base + hb * 64 + c * 32, lo, hi, p.n_sink,
-                                     bad >> (4 * hb + 2 * c)));
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float a0, a1, y0, y1;
@@ -855,14 +869,16 @@ __global__ void __launch_bounds__(512, 1)
             if (need || __all_sync(0xffffffffu, hsum < 32768.0f)) break;
             need = true;  // once: then P' is at most 2^kCacheBias
           }
+          if (gave_up) break;
           tmem_st_32cols(ts + hb * 32, pw);
           tsum += hsum;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull(half, hb));
         }
+        if (gave_up) break;
         l = fmaf(tsum, info.z, l);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(half));
       }
       if (!(flags & kTileLast)) continue;
       // ---- the segment's result: out, or a partial when the unit goes on elsewhere
@@ -878,44 +894,41 @@ __global__ void __launch_bounds__(512, 1)
       const float rl = m == -INFINITY ? 0.f : 1.0f / l;
       float* part = p.part + (2ll * blockIdx.x + (si.starts ? 1 : 0)) * C::kPartFloats;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint4 zw[4];
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t zz[8];
         if (gate) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) zw[q] = __ldg(zp + c * 4 + q);
+          const uint4 z0 = __ldg(zp + c * 2), z1 = __ldg(zp + c * 2 + 1);
+          zz[0] = z0.x, zz[1] = z0.y, zz[2] = z0.z, zz[3] = z0.w;
+          zz[4] = z1.x, zz[5] = z1.y, zz[6] = z1.z, zz[7] = z1.w;
         }
-        uint32_t o[32];
-        tmem_ld_32cols(to + c * 32, o);
+        uint32_t o[16];
+        tmem_ld_16cols(to + c * 16, o);
         tmem_wait_ld_of(o);
         if (whole) {
-          uint32_t w[2][8];
+          uint32_t w[8];
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
+          for (int q = 0; q < 8; ++q) {
             float x0 = __uint_as_float(o[2 * q]) * rl, x1 = __uint_as_float(o[2 * q + 1]) * rl;
             if (gate) {
-              const uint32_t zz = (&zw[q / 4].x)[q & 3];
-              x0 *= 1.0f / (1.0f + __expf(-bf16lo_to_f32(zz)));
-              x1 *= 1.0f / (1.0f + __expf(-bf16hi_to_f32(zz)));
+              x0 = __fdividef(x0, 1.0f + __expf(-bf16lo_to_f32(zz[q])));
+              x1 = __fdividef(x1, 1.0f + __expf(-bf16hi_to_f32(zz[q])));
             }
-            w[q >> 3][q & 7] = pack_bf16x2(x0, x1);
+            w[q] = pack_bf16x2(x0, x1);
           }
           if (have) {  // rows are 16-byte aligned, not always 32
-            uint4* op = reinterpret_cast<uint4*>(p.out + at + c * 32);
+            uint4* op = reinterpret_cast<uint4*>(p.out + at + c * 16);
             if ((reinterpret_cast<uintptr_t>(op) & 31) == 0) {
-              st_global_v8(op, w[0]);
-              st_global_v8(op + 2, w[1]);
+              st_global_v8(op, w);
             } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                op[q] = make_uint4(w[q >> 1][(q & 1) * 4], w[q >> 1][(q & 1) * 4 + 1],
-                                   w[q >> 1][(q & 1) * 4 + 2], w[q >> 1][(q & 1) * 4 + 3]);
+              op[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              op[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
         } else if (have) {
           // (rows that saw no key in this part hold zeros)
-          float* dst = part + (half * 128 + row) * D + c * 32;
+          float* dst = part + (half * 128 + row) * D + c * 16;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const uint32_t v[8] = {o[8 * q],     o[8 * q + 1], o[8 * q + 2], o[8 * q + 3],
                                    o[8 * q + 4], o[8 * q + 5], o[8 * q + 6], o[8 * q + 7]};
             st_global_v8(dst + q * 8, v);
