@@ -54,6 +54,17 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// One lane of a converged warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -444,8 +455,10 @@ __global__ void __launch_bounds__(512, 1)
   if (warp >= 12) {
     reg_dec<C::kIssuerRegs>();
     const int me = warp - 12;
-    if (me < 2 && lane == 0) {
+    if (me < 2) {
       // ---------------------------------------------------------- MMA issuers
+      // The whole warp walks the tiles, so that addresses and descriptors stay
+      // in uniform registers; one lane issues and commits.
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
       constexpr uint64_t kStep = C::kTileBytes >> 4;  // next buffer, in the address field
@@ -453,50 +466,59 @@ __global__ void __launch_bounds__(512, 1)
       const uint64_t kd = smem_desc(kbuf(0), 16, G::kGroupBytes, G::kLayout);
       const uint64_t vd = smem_desc(vbuf(0), G::kAtomTileBytes, G::kGroupBytes, G::kLayout);
       const uint32_t ts = tmem + me * 128, to = tmem + C::kAccO + me * D;
-      uint32_t seg = 0;
+      const bool lead = elect_one();
+      uint32_t seg = 0, flags = 0;
       auto issue_s = [&](uint32_t k) {  // S of tile k of this CTA
         if (!mbar_wait_idle(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
-        const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&s_info[k & kRing].flags);
+        flags = *reinterpret_cast<volatile uint32_t*>(&s_info[k & kRing].flags);
         if ((flags & kTileFirst) && !mbar_wait_idle(qfull, seg & 1u, abort, kCode)) return false;
         tc_fence_after();
         const uint64_t b0 = kd + (k & 1u) * kStep;
+        if (lead) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = ((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4;
-          mma_bf16(ts, qd + off, b0 + off, idesc_s, kk);
+          for (uint32_t kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = ((kk / KPA) * G::kAtomTileBytes + (kk % KPA) * 32) >> 4;
+            mma_bf16(ts, qd + off, b0 + off, idesc_s, kk);
+          }
+          mma_commit(sfull(me));
+          mma_commit(kempty(k & 1u));
+          if (flags & kTileLast) mma_commit(qempty);  // every S of the segment has been issued
         }
-        mma_commit(sfull(me));
-        mma_commit(kempty(k & 1u));
-        if (flags & kTileLast) mma_commit(qempty);  // every S of the segment has been issued
+        __syncwarp();
         return true;
       };
       bool ok = total > 0 && issue_s(0);
       for (uint32_t n = 0; n < total && ok; ++n) {
-        const uint32_t flags = *reinterpret_cast<volatile uint32_t*>(&s_info[n & kRing].flags);
-        if (((flags & kTileFirst) && !mbar_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
+        const uint32_t now = flags;  // of tile n
+        if (((now & kTileFirst) && !mbar_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
             !mbar_wait_idle(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
             !mbar_wait_idle(pfull(me, 0), n & 1u, abort, kCode))
           break;
         tc_fence_after();
         const uint64_t b0 = vd + (n & 1u) * kStep;
-        const uint32_t keep = (flags & kTileFirst) ? 0u : 1u;  // add to O, or begin it
+        const uint32_t keep = (now & kTileFirst) ? 0u : 1u;  // add to O, or begin it
+        if (lead) {
 #pragma unroll
-        for (uint32_t kk = 0; kk < 4; ++kk)  // 16 keys = 8 columns of P
-          mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, kk | keep);
-        mma_commit(pvdone(me));
+          for (uint32_t kk = 0; kk < 4; ++kk)  // 16 keys = 8 columns of P
+            mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, kk | keep);
+          mma_commit(pvdone(me));
+        }
+        __syncwarp();
         if (!mbar_wait_idle(pfull(me, 1), n & 1u, abort, kCode)) break;
         tc_fence_after();
+        if (lead) {
 #pragma unroll
-        for (uint32_t kk = 4; kk < 8; ++kk)
-          mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, 1u);
-        mma_commit(vempty(n & 1u));
-        if (flags & kTileLast) {
-          mma_commit(ofull(me));
-          ++seg;
+          for (uint32_t kk = 4; kk < 8; ++kk)
+            mma_bf16_ts(to, ts + kk * 8, b0 + kk * (2 * G::kGroupBytes >> 4), idesc_o, 1u);
+          mma_commit(vempty(n & 1u));
+          if (now & kTileLast) mma_commit(ofull(me));
         }
+        __syncwarp();
+        if (now & kTileLast) ++seg;
         if (n + 1 < total) ok = issue_s(n + 1);
       }
-      mma_commit(done_bar);
+      __syncwarp();
+      if (lead) mma_commit(done_bar);
       mbar_wait_drain(done_bar, 0);
     } else if (me == 2) {
       // ------------------------------------------------------------- producer
