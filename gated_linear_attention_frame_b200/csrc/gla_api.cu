@@ -1076,10 +1076,9 @@ int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t strea
 constexpr size_t kScheduleSmem = 160 * 1024;
 
 template <int D>
-int launch_combine(const gla::CacheAttnParams& p, int ctas, int part_floats, int rows,
-                   int half_rows, int used, cudaStream_t stream) {
+int launch_combine(const gla::CacheAttnParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, rows);
+  cfg.gridDim = dim3(ctas, gla::TokenCfg<D>::kRows);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1087,8 +1086,7 @@ int launch_combine(const gla::CacheAttnParams& p, int ctas, int part_floats, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p, part_floats, rows, half_rows,
-                         used) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p) != cudaSuccess) {
     cudaGetLastError();
     return GLA_ERR_LAUNCH;
   }
@@ -1110,7 +1108,7 @@ int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
   gla::gla_cache_token_kernel<D><<<grid, C::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) status = GLA_ERR_LAUNCH;
   if (status == GLA_OK) {
-    status = launch_combine<D>(p, grid, C::kPartFloats, C::kRows, C::kRows, C::kRows, stream);
+    status = launch_combine<D>(p, grid, stream);
   }
   if (cudaFreeAsync(ws, stream) != cudaSuccess) {
     cudaGetLastError();
@@ -1153,8 +1151,21 @@ int run_cache_frame(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
     cudaGetLastError();
     status = GLA_ERR_LAUNCH;
   }
-  if (status == GLA_OK)
-    status = launch_combine<D>(p, fs.ctas, C::kPartFloats, C::kRows, 128, fs.TQ * p.G, stream);
+  if (status == GLA_OK) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(fs.ctas, gla::kJoinBlocks);
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, gla::gla_cache_join_kernel<D>, p, fs.TQ * p.G) != cudaSuccess) {
+      cudaGetLastError();
+      status = GLA_ERR_LAUNCH;
+    }
+  }
   if (cudaFreeAsync(ws, stream) != cudaSuccess) {
     cudaGetLastError();
     if (status == GLA_OK) status = GLA_ERR_LAUNCH;

@@ -27,15 +27,14 @@
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).  One issuing
 // warp per half: P V of tile j (in two steps of 64 keys, as P is written), then
 // S of tile j + 1 into the same columns (the tensor core runs one thread's
-// products in order), while the other half's softmax runs; so the two halves
-// alternate between the tensor core and the exponentials.
+// products in order), while the other half's softmax runs.
 // Softmax: one thread per row.  P' = 2^(S f + lv - m + kCacheBias), f = key scale
 // x row scale x softmax scale x log2 e, lv = log2 of the value scale (taken out
 // of the row sum again).  The maximum of a tile is not taken as a rule: the
 // row's reference m stays while the sum of P' over 64 keys stays below 2^15
 // (then no P' leaves the fp16 range); otherwise, and on the first keys that a
 // row sees, they are read again, m becomes their maximum, and O is rescaled.
-// One pair of exponentials in four runs on the FMA pipe (exp2_poly3_x2).
+// (At d = 64 one pair of exponentials in four runs on the FMA pipe, exp2_poly3_x2.)
 // Warp roles: 0-3 / 4-7 softmax and epilogue of half 0 / 1, 8-11 converters,
 // 12 / 13 MMA issuers of half 0 / 1, 14 producer (15 idle: it completes the
 // register group).
@@ -200,7 +199,7 @@ struct FrameCfg {
   static constexpr int kSlots = 2;                  // K tiles and V tiles held each
   static constexpr int kInfoSlots = 8;
   static constexpr int kAccO = 256;
-  static constexpr int kBarCount = 4 * kSlots + 19;
+  static constexpr int kBarCount = 4 * kSlots + 27;
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kSlots * kTileBytes;
   static constexpr int kOffRs = kOffV + kSlots * kTileBytes;       // [2][256] row exponents
@@ -213,9 +212,18 @@ struct FrameCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
   static constexpr int kMinTiles = 4;  // least tiles of a CTA
+  // The two halves' softmax warps of one scheduler take turns (d = 128) or run
+  // as they come (d = 64).  Left alone, the halves fall into step: both in the
+  // softmax, then both on the tensor core.  Taking turns keeps one on each; a
+  // lone warp is then bound by its instructions, not by the exponential unit,
+  // so all exponentials go there.  Measured, turns / as they come with one pair
+  // of exponentials in four on the FMA pipe: 836 / 907 us (d = 128, 3680
+  // queries, 14720 keys, 24 heads), 381 / 359 us (d = 64 ragged prompts: half
+  // the tensor work, little to hide behind).
+  static constexpr bool kTurns = D == 128;
   // registers a thread: 128 at launch (512 threads); 256 softmax threads, 128
   // converters, 128 issuers and producer
-  static constexpr int kSoftmaxRegs = 168, kConverterRegs = 88, kIssuerRegs = 88;
+  static constexpr int kSoftmaxRegs = 160, kConverterRegs = 96, kIssuerRegs = 96;
   static_assert(256 * kSoftmaxRegs + 128 * (kConverterRegs + kIssuerRegs) <= 512 * 128,
                 "register shares beyond the launch's total would wait forever");
 };
@@ -409,6 +417,8 @@ __global__ void __launch_bounds__(512, 1)
   auto rfull = [&](int t) { return bar0 + 8u * (4 * S + 10 + t); };
   auto rempty = [&](int t) { return bar0 + 8u * (4 * S + 12 + t); };
   const uint32_t done_bar = bar0 + 8u * (4 * S + 14);
+  // whose turn it is: softmax warps q4 of the two halves (they share a scheduler)
+  auto turn = [&](int h, int q4) { return bar0 + 8u * (4 * S + 19 + 4 * h + q4); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBarCount);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(512, 1)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) mbar_init(turn(i >> 2, i & 3), 1);
     for (int s = 0; s < S; ++s) {
       mbar_init(kfull(s), 4);
       mbar_init(kempty(s), 2);
@@ -805,7 +816,9 @@ __global__ void __launch_bounds__(512, 1)
         const float fg = rs * info.x;
         const uint64_t f2 = f2_pack(fg, fg);
         float tsum = 0.f;
-        bool gave_up = false;
+        bool gave_up = C::kTurns && !warp_wait_idle(turn(half, q4), half == 0 ? (n & 1u) ^ 1u : n & 1u,
+                                                    abort, kCode);
+        if (gave_up) break;
 #pragma unroll 1
         for (int hb = 0; hb < 2; ++hb) {  // 64 keys at a time: their P' stays in 32 registers
           bool need = __any_sync(0xffffffffu, m == -INFINITY);  // take the maximum first
@@ -874,7 +887,7 @@ __global__ void __launch_bounds__(512, 1)
                 f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                  f2, s2),
                           a0, a1);
-                if ((e & 3) == 0) {
+                if (!C::kTurns && (e & 3) == 0) {
                   exp2_poly3_x2(a0, a1, y0, y1);
                 } else {
                   y0 = ex2_approx(a0);
@@ -894,6 +907,7 @@ __global__ void __launch_bounds__(512, 1)
           if (gave_up) break;
           tmem_st_32cols(ts + hb * 32, pw);
           tsum += hsum;
+          if (C::kTurns && hb == 1 && lane == 0) mbar_arrive(turn(half ^ 1, q4));
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -987,6 +1001,83 @@ __global__ void __launch_bounds__(512, 1)
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partials of a unit that several CTAs share, one warp a row: unit and
+// parts as in gla_cache_combine_kernel, which spends a block on a row (measured
+// over 148 split units of 256 rows: 33 us).  32 parts at a time: each lane takes
+// one part's (m, l), the weights go round by shuffle.
+constexpr int kJoinBlocks = 16;  // blocks a unit, four warps each
+
+template <int D>
+__global__ void __launch_bounds__(128)
+    gla_cache_join_kernel(const CacheAttnParams p, int used) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  using C = FrameCfg<D>;
+  constexpr int V = D / 32;  // columns of a lane
+  const int* desc = p.desc + 8 * blockIdx.x;
+  const int parts = desc[0];
+  if (parts == 0) return;
+  const int c0 = desc[1], unit_row = desc[2], h = desc[3], rows = desc[4];
+  const int lane = threadIdx.x & 31;
+  const int first = blockIdx.y * 4 + (threadIdx.x >> 5);
+  auto part_of = [&](int i) {
+    return p.part +
+           (i == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + i)) * C::kPartFloats;
+  };
+  for (int r = first; r < rows; r += kJoinBlocks * 4) {
+    const int rho = r < used ? r : 128 + (r - used);  // row of the partial
+    float m = -INFINITY, l = 0.f, acc[V] = {};
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < parts)
+        ml = *reinterpret_cast<const float2*>(part_of(i0 + lane) + C::kRows * D + 2 * rho);
+      float mn = fmaxf(m, ml.x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      if (mn == -INFINITY) continue;  // uniform
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+      float ls = ml.y * w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      m = mn;
+      l = l * f + ls;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= f;
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* x = part_of(i0 + i) + rho * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 o = __ldg(reinterpret_cast<const float4*>(x));
+          acc[0] = fmaf(o.x, wi, acc[0]);
+          acc[1] = fmaf(o.y, wi, acc[1]);
+          acc[2] = fmaf(o.z, wi, acc[2]);
+          acc[3] = fmaf(o.w, wi, acc[3]);
+        } else {
+          const float2 o = __ldg(reinterpret_cast<const float2*>(x));
+          acc[0] = fmaf(o.x, wi, acc[0]);
+          acc[1] = fmaf(o.y, wi, acc[1]);
+        }
+      }
+    }
+    const float rl = m == -INFINITY ? 0.f : 1.0f / l;
+    const int row = unit_row + r;
+    const int64_t off =
+        ((static_cast<int64_t>(c0) + row / p.G) * p.H + h * p.G + row % p.G) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      float x0 = acc[v] * rl, x1 = acc[v + 1] * rl;
+      if (p.z != nullptr) {
+        const uint32_t z = *reinterpret_cast<const uint32_t*>(p.z + off + v);
+        x0 *= 1.0f / (1.0f + __expf(-bf16lo_to_f32(z)));
+        x1 *= 1.0f / (1.0f + __expf(-bf16hi_to_f32(z)));
+      }
+      *reinterpret_cast<uint32_t*>(p.out + off + v) = pack_bf16x2(x0, x1);
+    }
   }
 }
 

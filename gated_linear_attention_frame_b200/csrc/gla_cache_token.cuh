@@ -677,21 +677,18 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
 // Joins the partials of a unit that several CTAs share: CTA x of the grid takes
 // the unit (if any) that begins in CTA x of the attention kernel and goes on
 // after it; its parts are partial 1 of that CTA and partial 0 of the next
-// ones.  blockIdx.y: a query row of the unit; of every `half_rows` rows the first
-// `used` hold queries.  Four (eight at d = 64) groups of threads
+// ones.  blockIdx.y: a query row.  Four (eight at d = 64) groups of threads
 // take every fourth (eighth) part; the sums are joined in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnParams p,
-                                                                int part_floats, int part_rows,
-                                                                int half_rows, int used) {
+__global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kGroups = 128 / (D / 4);
+  constexpr int part_floats = TokenCfg<D>::kPartFloats, part_rows = TokenCfg<D>::kRows;
   __shared__ float4 s_acc[128];
   __shared__ float s_m[kGroups], s_l[kGroups];
   const int* desc = p.desc + 8 * blockIdx.x;
   const int parts = desc[0], rho = blockIdx.y;
-  const int in_unit = rho / half_rows * used + rho % half_rows;
-  if (parts == 0 || rho % half_rows >= used || in_unit >= desc[4]) return;
+  if (parts == 0 || rho >= desc[4]) return;
   const int grp = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
   auto part_of = [&](int i) {
     return p.part + (i == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + i)) * part_floats;
@@ -735,7 +732,7 @@ __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnP
     o.w += x.w * f;
   }
   const float rl = mm == -INFINITY ? 0.f : 1.0f / l;
-  const int row = desc[2] + in_unit;
+  const int row = desc[2] + rho;
   const int64_t off =
       ((static_cast<int64_t>(desc[1]) + row / p.G) * p.H + desc[3] * p.G + row % p.G) * D + c4 * 4;
   float x[4] = {o.x * rl, o.y * rl, o.z * rl, o.w * rl};
