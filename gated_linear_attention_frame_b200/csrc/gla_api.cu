@@ -1121,7 +1121,7 @@ template <int D>
 int run_cache_frame(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t stream) {
   using C = gla::FrameCfg<D>;
   gla::FrameSchedule fs{};
-  fs.ctas = di.sms;
+  fs.ctas = di.sms < gla::kMaxScheduleCtas ? di.sms : gla::kMaxScheduleCtas;
   fs.TQ = 128 / p.G;
   fs.entries_max = p.tokens / (2 * fs.TQ) + p.R;
   const size_t e0_bytes = (static_cast<size_t>(p.R + 1) * 4 + 15) / 16 * 16;
@@ -1203,9 +1203,12 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;
+  p.tile_t = p.G <= 16 ? 16 / p.G : 1;
+  p.tile_c = p.G <= 16 ? 1 : (p.G + 15) / 16;
   // up to 64 query rows of a sequence and head: the keys are read (row tiles)
-  // times; more fill the 128-row tiles of the tensor cores
-  if (static_cast<int64_t>(max_new) * p.G <= 64)
+  // times; more fill the 128-row tiles of the tensor cores.  (The token
+  // kernel's tile numbers are 32-bit.)
+  if (static_cast<int64_t>(max_new) * p.G <= 64 && p.tokens <= (1 << 27))
     return d == 64 ? run_cache_token<64>(p, di, stream) : run_cache_token<128>(p, di, stream);
   return d == 64 ? run_cache_frame<64>(p, di, stream) : run_cache_frame<128>(p, di, stream);
 }

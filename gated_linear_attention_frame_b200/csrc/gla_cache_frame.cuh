@@ -137,10 +137,6 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
                : "memory");
 }
 
-// i / G for 0 <= i < 256 and 1 <= G <= 128, with m = (65536 + G - 1) / G (checked
-// for every i and G).
-__device__ __forceinline__ int small_div(int i, int m) { return (i * m) >> 16; }
-
 // 32-byte global accesses, a whole sector for each lane.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
@@ -228,6 +224,10 @@ struct FrameCfg {
                 "register shares beyond the launch's total would wait forever");
 };
 
+constexpr int kMaxScheduleCtas = 1024;
+constexpr int kJoinTiles = 6;  // what writing and joining partials costs, in tiles (measured at
+                               // d = 128: about 17 us and 2.9 us)
+
 // Where the schedule goes: starts[c] = {sequence, kv head, unit, tile} of the
 // first tile of CTA c and n[c] its number of tiles.
 struct FrameSchedule {
@@ -293,29 +293,55 @@ __global__ void __launch_bounds__(1024, 1)
   const long long tiles = total * p.Hkv;
   const long long want = (tiles + FrameCfg<D>::kMinTiles - 1) / FrameCfg<D>::kMinTiles;
   const int ctas = static_cast<int>(want < fs.ctas ? want : fs.ctas);
+  // unit of tile x0 (order: sequence, kv head, unit) and the tile within it
+  auto find = [&](long long x0, int& tiles_of_unit) {
+    int lo = 0, hi = p.R;  // sequence: tiles before lo <= x0 < tiles before hi
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[e0[mid]] * p.Hkv <= x0)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const long long base = pre[e0[lo]];
+    const long long one = pre[e0[lo + 1]] - base;  // tiles of one kv head
+    const long long x = x0 - base * p.Hkv;
+    int4 st;
+    st.x = lo;
+    st.y = static_cast<int>(x / one);
+    const long long in_head = x % one + base;
+    st.z = prefix_owner<long long>(pre + e0[lo], e0[lo + 1] - e0[lo], in_head);
+    st.w = static_cast<int>(in_head - pre[e0[lo] + st.z]);
+    tiles_of_unit = static_cast<int>(pre[e0[lo] + st.z + 1] - pre[e0[lo] + st.z]);
+    return st;
+  };
+  // Equal shares, cut anywhere; or, where that costs no CTA more than
+  // kJoinTiles tiles, the same shares cut at the nearest unit (no partials, no
+  // join).
+  __shared__ long long s_cut[kMaxScheduleCtas + 1];
+  int over = 0;
+  for (int c = tid; c <= ctas; c += 1024) {
+    long long x = share_lo(tiles, ctas, c);
+    if (c > 0 && c < ctas) {
+      int nt;
+      const int4 st = find(x, nt);
+      x += 2 * st.w >= nt ? nt - st.w : -st.w;
+    }
+    s_cut[c] = x;
+  }
+  __syncthreads();
+  const long long share = ctas > 0 ? (tiles + ctas - 1) / ctas : 0;
+  for (int c = tid; c < ctas; c += 1024) over |= s_cut[c + 1] - s_cut[c] > share + kJoinTiles;
+  const bool cut = __syncthreads_or(over);
   for (int c = tid; c < fs.ctas; c += 1024) {
     int4 st = make_int4(0, 0, 0, 0);
     int n = 0;
     if (c < ctas) {
-      const long long x0 = share_lo(tiles, ctas, c);
-      n = static_cast<int>(share_lo(tiles, ctas, c + 1) - x0);
-      int lo = 0, hi = p.R;  // sequence: tiles before lo <= x0 < tiles before hi
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[e0[mid]] * p.Hkv <= x0)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const long long base = pre[e0[lo]];
-      const long long one = pre[e0[lo + 1]] - base;  // tiles of one kv head
-      long long x = x0 - base * p.Hkv;
-      st.x = lo;
-      st.y = static_cast<int>(x / one);
-      x = x % one + base;
-      const int nu = e0[lo + 1] - e0[lo];
-      st.z = prefix_owner<long long>(pre + e0[lo], nu, x);
-      st.w = static_cast<int>(x - pre[e0[lo] + st.z]);
+      const long long x0 = cut ? share_lo(tiles, ctas, c) : s_cut[c];
+      const long long x1 = cut ? share_lo(tiles, ctas, c + 1) : s_cut[c + 1];
+      int nt;
+      n = static_cast<int>(x1 - x0);
+      if (n > 0) st = find(x0, nt);
     }
     fs.starts[c] = st;
     fs.n[c] = n;

@@ -49,6 +49,9 @@ struct CacheAttnParams {
   int pages, max_pages, p_shift;  // P = 1 << p_shift
   int F, W, n_sink;
   float sl2;  // scale * log2(e)
+  // token kernel: a tile of 16 rows holds `tile_t` tokens (all G heads of each),
+  // or, where G > 16, one of `tile_c` parts of one token's heads
+  int tile_t, tile_c;
   // split units: per CTA two partials of kPartRows rows (fp32 O, then m, l)
   // and one descriptor
   float* part;
@@ -128,6 +131,10 @@ __device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
   return up > 126 ? 126 : up;
 }
 
+// i / G for 0 <= i < 256 and 1 <= G <= 128, with m = (65536 + G - 1) / G (checked
+// for every i and G).
+__device__ __forceinline__ int small_div(int i, int m) { return (i * m) >> 16; }
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -198,18 +205,22 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kRingBytes + C::kMergeBytes);
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kFixedBytes);  // [R + 1]
   __shared__ long long scratch[33];
+  __shared__ float2 s_row[8];  // (m, l) of the rows on their way out
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int P = 1 << p.p_shift;
 
-  // rows of a sequence in tiles of 16, and the blocks before each sequence
+  // query tiles of a sequence, and the keys one of them sees
+  const int gm = (65536 + p.G - 1) / p.G;  // see small_div
   auto tiles_of = [&](const CacheSeq& s) {
-    return static_cast<int>((static_cast<int64_t>(s.n) * p.G + 15) >> 4);
+    return p.tile_c > 1 ? s.n * p.tile_c : (s.n + p.tile_t - 1) / p.tile_t;
+  };
+  auto first_token = [&](int tile) {
+    return p.tile_c > 1 ? tile / p.tile_c : tile * p.tile_t;
   };
   auto span_of = [&](const CacheSeq& s, int tile) {
-    const int t_lo = tile * 16 / p.G;
-    const int t_hi = min(static_cast<int>((static_cast<int64_t>(tile) * 16 + 15) / p.G), s.n - 1);
-    return cache_span<BK>(p, s, t_lo, t_hi);
+    const int t = first_token(tile);
+    return cache_span<BK>(p, s, t, min(t + p.tile_t, s.n) - 1);
   };
   auto blocks_of = [&](int r) -> long long {
     const CacheSeq s = cache_seq(p, r);
@@ -351,27 +362,31 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
     }
     cp_async_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int s = 0; s < C::kStages; ++s) issue(s);
   int st = 0;
 
   for (; cur.live; next_unit(cur)) {
-    const int rows = min(16, static_cast<int>(static_cast<int64_t>(cur.s.n) * p.G -
-                                              static_cast<int64_t>(cur.tile) * 16));
+    // rows of the tile: token t0 + row / G, head g0 + row % G of the group
+    const int t0 = first_token(cur.tile);
+    const int g0 = p.tile_c > 1 ? (cur.tile - t0 * p.tile_c) * 16 : 0;
+    const int rows = p.tile_c > 1 ? min(16, p.G - g0) : min(p.tile_t, cur.s.n - t0) * p.G;
+    const int64_t row0 =
+        (static_cast<int64_t>(cur.s.c0) + t0) * p.H + cur.h * p.G + g0;  // of q and out
+    auto row_token = [&](int rho) { return p.tile_c > 1 ? 0 : small_div(rho, gm); };
     // ---- query fragments: rows g and g + 8 of the tile
     uint32_t qa[D / 16][4];
     float rs[2];                 // undoes the row scale, times scale log2(e)
     int hi[2], lo[2];
-    int64_t qoff[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int rho = g + 8 * e;
       const bool have = rho < rows;
-      const int64_t rr = static_cast<int64_t>(cur.tile) * 16 + (have ? rho : 0);
-      const int t = static_cast<int>(rr / p.G), hq = static_cast<int>(rr % p.G);
-      qoff[e] = ((static_cast<int64_t>(cur.s.c0) + t) * p.H + cur.h * p.G + hq) * D;
-      hi[e] = have ? key_hi(p, cur.s, cur.s.p0 + t) : 0;
-      lo[e] = key_lo(p, cur.s.p0 + t);
+      const int rt = have ? row_token(rho) : 0;
+      const __nv_bfloat16* qp =
+          p.q + (row0 + static_cast<int64_t>(rt) * p.H + (have ? rho - rt * p.G : 0)) * D;
+      hi[e] = have ? key_hi(p, cur.s, cur.s.p0 + t0 + rt) : 0;
+      lo[e] = key_lo(p, cur.s.p0 + t0 + rt);
       uint4 w[KI][2];
       uint32_t mx = 0;
 #pragma unroll
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
         for (int f = 0; f < 2; ++f) {
           w[i][f] = make_uint4(0, 0, 0, 0);
           if (have)
-            w[i][f] = *reinterpret_cast<const uint4*>(p.q + qoff[e] + i * 64 + t4 * 16 + f * 8);
+            w[i][f] = *reinterpret_cast<const uint4*>(qp + i * 64 + t4 * 16 + f * 8);
           mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[i][f].x & 0x7FFF7FFFu, w[i][f].y & 0x7FFF7FFFu),
                                      __vmaxu2(w[i][f].z & 0x7FFF7FFFu, w[i][f].w & 0x7FFF7FFFu)));
         }
@@ -405,8 +420,8 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
     for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     // every row sees every key of a block inside [all_lo, all_hi)
-    const int all_hi = key_hi(p, cur.s, cur.s.p0 + static_cast<int>(static_cast<int64_t>(cur.tile) * 16 / p.G));
-    const int all_lo = key_lo(p, cur.s.p0 + static_cast<int>((static_cast<int64_t>(cur.tile) * 16 + rows - 1) / p.G));
+    const int all_hi = key_hi(p, cur.s, cur.s.p0 + t0);
+    const int all_lo = key_lo(p, cur.s.p0 + t0 + row_token(rows - 1));
 
     for (; cur.k < cur.k_end; cur.k += C::kWarps) {
       cp_async_wait<C::kStages - 1>();
@@ -581,6 +596,10 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       }
     }
     const bool low = rows > 8;  // rows g + 8 hold something (uniform)
+    const bool starts = cur.k0 == 0, ends = cur.k_end == cur.v.nb, whole = starts && ends;
+    // the CTA's first part of a unit begun before it goes to its partial 0, a
+    // unit that goes on after it to partial 1
+    float* part = p.part + (2ll * blockIdx.x + (starts ? 1 : 0)) * C::kPartFloats;
     auto slot = [&](int buf, int n, int x) -> float& {
       return s_o[((buf * 2 * NT) + n * 2 + x) * 32 + lane];
     };
@@ -610,65 +629,65 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
           }
         }
       }
-    }
-    const bool starts = cur.k0 == 0, ends = cur.k_end == cur.v.nb;
-    if (warp == 0) {
+      // warp 0 holds the sums: through shared memory once more, so that all
+      // threads write whole row pieces of 8 columns
+      if (warp == 0) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rho = g + 8 * e;
+        for (int n = 0; n < NT; ++n) {
+          slot(0, n, 0) = o[n][2 * e];
+          slot(0, n, 1) = o[n][2 * e + 1];
+        }
+        if (t4 == 0) s_row[g] = make_float2(mm[e], ll[e]);
+      }
+      __syncthreads();
+      constexpr int kPieces = D / 8;  // of a row
+#pragma unroll 1
+      for (int i = tid; i < 8 * kPieces; i += C::kThreads) {
+        const int r8 = i / kPieces, c = i % kPieces, rho = r8 + 8 * e;
         if (rho >= rows) continue;
-        constexpr int kCols = D / 4;  // columns of this thread
-        if (starts && ends) {
-          const float rl = mm[e] == -INFINITY ? 0.f : 1.0f / ll[e];
-          __nv_bfloat16* dst = p.out + qoff[e] + t4 * kCols;
-          const __nv_bfloat16* zs = p.z != nullptr ? p.z + qoff[e] + t4 * kCols : nullptr;
+        // columns 8 c .. 8 c + 7: thread (r8, col / (D / 4)), its n-tiles col % NT
+        // of half (col / NT) & 1
+        const int t = c * 8 / (D / 4), x = (c * 8 / NT) & 1, n0 = c * 8 % NT;
+        float v[8];
 #pragma unroll
-          for (int c = 0; c < kCols / 8; ++c) {
-            float x[8];
+        for (int y = 0; y < 8; ++y) v[y] = s_o[((n0 + y) * 2 + x) * 32 + r8 * 4 + t];
+        const float2 ml = s_row[r8];
+        if (whole) {
+          const int rt = row_token(rho);
+          const int64_t at =
+              (row0 + static_cast<int64_t>(rt) * p.H + (rho - rt * p.G)) * D + c * 8;
+          const float rl = ml.x == -INFINITY ? 0.f : 1.0f / ml.y;
+          uint4 zw = make_uint4(0, 0, 0, 0);
+          if (p.z != nullptr) zw = *reinterpret_cast<const uint4*>(p.z + at);
+          const uint32_t zz[4] = {zw.x, zw.y, zw.z, zw.w};
+          uint32_t w[4];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const int col = c * 8 + y;  // column col of the thread: n-tile col % NT
-              x[y] = o[col % NT][2 * e + col / NT] * rl;
+          for (int y = 0; y < 4; ++y) {
+            float a = v[2 * y] * rl, b = v[2 * y + 1] * rl;
+            if (p.z != nullptr) {
+              a = __fdividef(a, 1.0f + __expf(-bf16lo_to_f32(zz[y])));
+              b = __fdividef(b, 1.0f + __expf(-bf16hi_to_f32(zz[y])));
             }
-            if (zs != nullptr) {
-              const uint4 zw = *reinterpret_cast<const uint4*>(zs + c * 8);
-              const uint32_t zz[4] = {zw.x, zw.y, zw.z, zw.w};
-#pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const float zf =
-                    (y & 1) ? bf16hi_to_f32(zz[y >> 1]) : bf16lo_to_f32(zz[y >> 1]);
-                x[y] *= 1.0f / (1.0f + expf(-zf));
-              }
-            }
-            *reinterpret_cast<uint4*>(dst + c * 8) =
-                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                           pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            w[y] = pack_bf16x2(a, b);
           }
+          *reinterpret_cast<uint4*>(p.out + at) = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-          // the CTA's first part of a unit begun before it goes to its
-          // partial 0, a unit that goes on after it to partial 1
-          float* part = p.part + (2ll * blockIdx.x + (starts ? 1 : 0)) * C::kPartFloats;
-          float* dst = part + rho * D + t4 * kCols;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 4)
-            *reinterpret_cast<float4*>(dst + c) =
-                make_float4(o[c % NT][2 * e + c / NT], o[(c + 1) % NT][2 * e + (c + 1) / NT],
-                            o[(c + 2) % NT][2 * e + (c + 2) / NT],
-                            o[(c + 3) % NT][2 * e + (c + 3) / NT]);
-          if (t4 == 0)
-            *reinterpret_cast<float2*>(part + 16 * D + 2 * rho) = make_float2(mm[e], ll[e]);
+          float4* dst = reinterpret_cast<float4*>(part + rho * D + c * 8);
+          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (c == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * rho) = ml;
         }
       }
-      if (lane == 0 && starts && !ends) {
-        int parts = 1;
-        const long long x_end = cur.x_unit + cur.v.nb;
-        for (int c = blockIdx.x + 1; c < ctas && share_lo(total, ctas, c) < x_end; ++c) ++parts;
-        desc[1] = cur.s.c0;
-        desc[2] = cur.tile * 16;
-        desc[3] = cur.h;
-        desc[4] = rows;
-        desc[0] = parts;
-      }
+    }
+    if (tid == 0 && starts && !ends) {
+      int parts = 1;
+      const long long x_end = cur.x_unit + cur.v.nb;
+      for (int c = blockIdx.x + 1; c < ctas && share_lo(total, ctas, c) < x_end; ++c) ++parts;
+      desc[1] = cur.s.c0 + t0;
+      desc[2] = g0;
+      desc[3] = cur.h;
+      desc[4] = rows;
+      desc[0] = parts;
     }
   }
   cp_async_wait<0>();
@@ -732,9 +751,9 @@ __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnP
     o.w += x.w * f;
   }
   const float rl = mm == -INFINITY ? 0.f : 1.0f / l;
-  const int row = desc[2] + rho;
+  const int g = desc[2] + rho, rt = g / p.G;  // g0 = 0 unless a token has several tiles
   const int64_t off =
-      ((static_cast<int64_t>(desc[1]) + row / p.G) * p.H + desc[3] * p.G + row % p.G) * D + c4 * 4;
+      ((static_cast<int64_t>(desc[1]) + rt) * p.H + desc[3] * p.G + (g - rt * p.G)) * D + c4 * 4;
   float x[4] = {o.x * rl, o.y * rl, o.z * rl, o.w * rl};
   if (p.z != nullptr) {
     const uint2 zw = *reinterpret_cast<const uint2*>(p.z + off);
