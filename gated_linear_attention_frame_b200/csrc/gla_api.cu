@@ -190,10 +190,30 @@ cudaError_t set_smem_attrs() {
 }
 
 cudaError_t set_cache_attrs() {
-  cudaError_t e = cudaFuncSetAttribute(gla::gla_cache_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (4 * gla::kCacheMaxSeqs + 3) * 4);
+  constexpr int kPlan = (4 * gla::kCacheMaxSeqs + 3) * 4;
+  cudaError_t e = cudaFuncSetAttribute(gla::gla_cache_plan_kernel<true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kPlan);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gla::gla_cache_plan_kernel<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kPlan);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(gla::gla_cache_slots_kernel,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kPlan);
+  if (e != cudaSuccess) return e;
+  const void* store[] = {
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<64, 16>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<64, 32>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<64, 64>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<64, 128>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<128, 16>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<128, 32>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<128, 64>),
+      reinterpret_cast<const void*>(gla::gla_cache_store_kernel<128, 128>)};
+  for (const void* f : store) {
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (3 * gla::kCacheMaxSeqs + 2) * 4);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int kPre = (gla::kCacheMaxSeqs + 1) * 8;
   e = cudaFuncSetAttribute(gla::gla_cache_token_kernel<64>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -990,11 +1010,13 @@ int validate_cache_window(int F, int W, int n_sink) {
   return (F < 1 || W < 0 || n_sink < 0) ? GLA_ERR_SHAPE : GLA_OK;
 }
 
-int cache_plan_impl(const gla::PlanParams& p, cudaStream_t stream) {
-  int st = validate_cache(p.R, p.tokens, p.pages, p.P);
+int page_shift(int P) { return P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7; }
+
+int cache_plan_impl(gla::PlanParams p, int P, cudaStream_t stream) {
+  int st = validate_cache(p.R, p.tokens, p.pages, P);
   if (st != GLA_OK) return st;
   if ((st = validate_cache_window(p.F, p.W, p.n_sink)) != GLA_OK) return st;
-  if (p.max_pages < 0 || static_cast<int64_t>(p.max_pages) * p.P > INT32_MAX) return GLA_ERR_SHAPE;
+  if (p.max_pages < 0 || static_cast<int64_t>(p.max_pages) * P > INT32_MAX) return GLA_ERR_SHAPE;
   if (p.free_count == nullptr || p.free_count_out == nullptr || p.cu == nullptr ||
       p.status == nullptr)
     return GLA_ERR_NULL;
@@ -1008,24 +1030,24 @@ int cache_plan_impl(const gla::PlanParams& p, cudaStream_t stream) {
                        p.lens_out, p.held_out, p.free_count_out, p.cu, p.slots, p.status};
   for (const void* x : all)
     if (!aligned(x, 4)) return GLA_ERR_ALIGN;
+  p.p_shift = page_shift(P);
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;
-  // one CTA up to 8192 tokens and 1024 sequences (its launch is the shorter
-  // one), the largest portable cluster above
-  const int ctas = p.tokens > 8192 || p.R > gla::kPlanThreads ? 8 : 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(gla::kPlanThreads);
-  cfg.dynamicSmemBytes = (4 * static_cast<size_t>(p.R) + 3) * sizeof(int);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_plan_kernel, p) != cudaSuccess) {
+  const size_t smem = (4 * static_cast<size_t>(p.R) + 3) * sizeof(int);
+  // up to 8192 tokens (two rounds of the one CTA) a single launch; more go to
+  // a second one over the whole GPU
+  if (p.tokens <= 8192) {
+    gla::gla_cache_plan_kernel<true><<<1, gla::kPlanThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+  }
+  gla::gla_cache_plan_kernel<false><<<1, gla::kPlanThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return GLA_ERR_LAUNCH;
+  const int64_t want = (static_cast<int64_t>(p.tokens) + 4 * gla::kSlotThreads - 1) /
+                       (4 * gla::kSlotThreads);
+  const unsigned grid = static_cast<unsigned>(want < 2 * di.sms ? want : 2 * di.sms);
+  if (launch_dependent(gla::gla_cache_slots_kernel, grid, static_cast<unsigned>(gla::kSlotThreads),
+                       (3 * static_cast<size_t>(p.R) + 2) * sizeof(int), stream,
+                       p) != cudaSuccess) {
     cudaGetLastError();
     return GLA_ERR_LAUNCH;
   }
@@ -1033,13 +1055,17 @@ int cache_plan_impl(const gla::PlanParams& p, cudaStream_t stream) {
 }
 
 using StoreKernel = void (*)(const gla::StoreParams);
+struct StoreChoice {
+  StoreKernel fn;
+  int per_sm;
+};
 template <int D>
-StoreKernel store_kernel(int P) {
+StoreChoice store_kernel(int P) {
   switch (P) {
-    case 16: return gla::gla_cache_store_kernel<D, 16>;
-    case 32: return gla::gla_cache_store_kernel<D, 32>;
-    case 64: return gla::gla_cache_store_kernel<D, 64>;
-    default: return gla::gla_cache_store_kernel<D, 128>;
+    case 16: return {gla::gla_cache_store_kernel<D, 16>, gla::StoreCfg<D, 16>::kPerSm};
+    case 32: return {gla::gla_cache_store_kernel<D, 32>, gla::StoreCfg<D, 32>::kPerSm};
+    case 64: return {gla::gla_cache_store_kernel<D, 64>, gla::StoreCfg<D, 64>::kPerSm};
+    default: return {gla::gla_cache_store_kernel<D, 128>, gla::StoreCfg<D, 128>::kPerSm};
   }
 }
 
@@ -1063,11 +1089,11 @@ int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t strea
   // at most one item for each page the tokens can touch, head and tensor
   const int64_t runs = static_cast<int64_t>(p.tokens) / P + 2 * static_cast<int64_t>(p.R);
   const int64_t items = (runs < p.tokens ? runs : p.tokens) * p.H * 2;
-  const int64_t most = static_cast<int64_t>(di.sms) * 16;
+  const StoreChoice k = d == 64 ? store_kernel<64>(P) : store_kernel<128>(P);
+  const int64_t most = static_cast<int64_t>(di.sms) * k.per_sm;
   const int grid = static_cast<int>(items < most ? items : most);
-  const size_t smem = (static_cast<size_t>(p.R) + 1) * sizeof(int);
-  StoreKernel fn = d == 64 ? store_kernel<64>(P) : store_kernel<128>(P);
-  fn<<<grid, gla::kStoreThreads, smem, stream>>>(p);
+  const size_t smem = (3 * static_cast<size_t>(p.R) + 2) * sizeof(int);
+  k.fn<<<grid, gla::kStoreThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
@@ -1198,7 +1224,7 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   for (const void* x : small)
     if (!aligned(x, 4)) return GLA_ERR_ALIGN;
   p.G = p.H / p.Hkv;
-  p.p_shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
+  p.p_shift = page_shift(P);
   p.sl2 = static_cast<float>(1.4426950408889634 * scale);
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;
@@ -1395,11 +1421,11 @@ int gla_cache_plan(const int* lens, const int* held, const int* new_lens, const 
                    int* free_count_out, int* cu_tokens, int* slots, int* status, int R,
                    int max_pages, int pages, int page_tokens, int tokens, int frame_tokens,
                    int window_frames, int n_sink, cudaStream_t stream) {
-  gla::PlanParams p{lens,     held,           new_lens,  free_count, free_pages,  block_table,
-                    lens_out, held_out,       free_count_out, cu_tokens, slots, status,
-                    R,        max_pages,      pages,     page_tokens, tokens,     frame_tokens,
+  gla::PlanParams p{lens,     held,      new_lens, free_count,     free_pages, block_table,
+                    lens_out, held_out,  free_count_out, cu_tokens, slots,    status,
+                    R,        max_pages, pages,    0,              tokens,     frame_tokens,
                     window_frames, n_sink};
-  return cache_plan_impl(p, stream);
+  return cache_plan_impl(p, page_tokens, stream);
 }
 
 int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu_tokens,

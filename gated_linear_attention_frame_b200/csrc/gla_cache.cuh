@@ -18,10 +18,6 @@ namespace gla {
 constexpr int kCacheMaxSeqs = 8192;   // sequences of one call (their prefix sums sit in shared
                                       // memory)
 
-__host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) {
-  return (a + b - 1) / b;
-}
-
 // First index of `a[0 .. n]` (ascending, a[0] = 0) whose successor exceeds x:
 // the owner of item x of a prefix sum.  0 <= x < a[n].
 template <typename T>
@@ -38,33 +34,47 @@ __device__ __forceinline__ int prefix_owner(const T* a, int n, T x) {
 }
 
 // Exclusive prefix sums over the threads of a block (whole warps, at most
-// 1024 threads); `total` is the sum over all of them.  `scratch`: 33 values.
-// Ends with every thread past its reads of `scratch`.
-template <typename T>
-__device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T& total) {
+// 1024 threads) of N values at once; `total` are the sums over all of them.
+// `scratch`: 33 N values.  Ends with every thread past its reads of `scratch`.
+template <int N, typename T>
+__device__ __forceinline__ void block_exclusive_scan_n(T (&v)[N], T (*scratch)[33], T (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  T x = v;
+  T x[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+  for (int i = 0; i < N; ++i) {
+    x[i] = v[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, x[i], o);
+      if (lane >= o) x[i] += y;
+    }
+    if (lane == 31) scratch[i][warp] = x[i];
   }
-  if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    T w = lane < warps ? scratch[lane] : T(0);
+  if (warp < N) {
+    T w = lane < warps ? scratch[warp][lane] : T(0);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
-    scratch[lane] = w;
+    scratch[warp][lane] = w;
   }
   __syncthreads();
-  const T base = warp > 0 ? scratch[warp - 1] : T(0);
-  total = scratch[warps - 1];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = (warp > 0 ? scratch[i][warp - 1] : T(0)) + x[i] - v[i];
+    total[i] = scratch[i][warps - 1];
+  }
   __syncthreads();
-  return base + x - v;
+}
+
+template <typename T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T& total) {
+  T x[1] = {v}, all[1];
+  block_exclusive_scan_n<1, T>(x, reinterpret_cast<T(*)[33]>(scratch), all);
+  total = all[0];
+  return x[0];
 }
 
 // ------------------------------------------------------------------- plan
@@ -72,193 +82,234 @@ __device__ __forceinline__ T block_exclusive_scan(T v, T* scratch, T& total) {
 struct PlanParams {
   const int *lens, *held, *new_lens, *free_count;
   int *free_pages, *table, *lens_out, *held_out, *free_count_out, *cu, *slots, *status;
-  int R, max_pages, pages, P, tokens, F, W, n_sink;
+  int R, max_pages, pages, p_shift, tokens, F, W, n_sink;  // P = 1 << p_shift
 };
 
 constexpr int kPlanThreads = 1024;
 
 // The pages of one sequence in this step.
 struct PlanSeq {
-  int64_t L, n;        // cached tokens, new tokens (0 for a finished sequence)
-  int64_t np_old, np_new;
-  int64_t held_out;
-  int64_t sink_back;   // finished: pages 0 .. sink_back - 1 go back too
-  int64_t back_lo, back_hi;
+  int L, n;             // cached tokens, new tokens (0 for a finished sequence)
+  int np_old;           // pages held before and after the step, but for the window
+  int64_t np_new;
+  int held_out;
+  int sink_back;        // finished: pages 0 .. sink_back - 1 go back too
+  int back_lo, back_hi;
   bool done;
-  __device__ int64_t back() const { return sink_back + back_hi - back_lo; }
+  __device__ int64_t back() const { return static_cast<int64_t>(sink_back) + back_hi - back_lo; }
 };
+
+__device__ __forceinline__ int pages_of(int64_t tokens, int p_shift) {
+  return static_cast<int>((tokens + (1 << p_shift) - 1) >> p_shift);
+}
 
 __device__ __forceinline__ PlanSeq plan_seq(const PlanParams& p, int r) {
   PlanSeq s;
-  s.L = p.lens[r] > 0 ? p.lens[r] : 0;
-  const int64_t nl = p.new_lens[r];
-  const int64_t held = p.held[r] > 0 ? p.held[r] : 0;
+  s.L = max(p.lens[r], 0);
+  const int nl = p.new_lens[r];
+  const int held = max(p.held[r], 0);
   s.done = nl < 0;
   s.n = s.done ? 0 : nl;
-  const int64_t sp = ceil_div64(p.n_sink, p.P);
-  s.np_old = ceil_div64(s.L, p.P);
-  s.np_new = s.done ? s.np_old : ceil_div64(s.L + s.n, p.P);
-  int64_t low = 0;
+  const int sp = pages_of(p.n_sink, p.p_shift);
+  s.np_old = pages_of(s.L, p.p_shift);
+  s.np_new = s.done ? s.np_old
+                    : (static_cast<int64_t>(s.L) + s.n + (1 << p.p_shift) - 1) >> p.p_shift;
+  int low = 0;
   if (p.W > 0) {
-    const int64_t w_lo = (s.L / p.F - p.W + 1) * p.F;
-    low = w_lo > 0 ? w_lo / p.P : 0;
+    const int64_t w_lo = (static_cast<int64_t>(s.L / p.F) - p.W + 1) * p.F;
+    low = w_lo > 0 ? static_cast<int>(w_lo >> p.p_shift) : 0;
   }
-  const int64_t upto = s.done ? s.np_old : (held > low ? held : low);
+  const int upto = s.done ? s.np_old : max(held, low);
   s.held_out = s.done ? 0 : upto;
-  s.back_lo = held > sp ? held : sp;
-  s.back_hi = upto > s.back_lo ? upto : s.back_lo;
-  s.sink_back = s.done ? (s.np_old < sp ? s.np_old : sp) : 0;
+  s.back_lo = max(held, sp);
+  s.back_hi = max(upto, s.back_lo);
+  s.sink_back = s.done ? min(s.np_old, sp) : 0;
   return s;
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+// Slots of four neighbouring tokens 4 q .. 4 q + 3 (one search, then a walk along
+// the sequences), and the table entries of the pages that begin there.  cu and
+// need: prefix sums of the new tokens and new pages; len(r): tokens of sequence
+// r before the step; top: stack entry of the first new page.
+template <typename Len>
+__device__ __forceinline__ void plan_slots(const PlanParams& p, int q, int tokens, const int* cu,
+                                           const int* need, int top, Len len) {
+  int out[4] = {-1, -1, -1, -1};
+  const int i0 = q * 4;
+  if (i0 < tokens) {
+    int r = prefix_owner<int>(cu, p.R, i0);
+    int L = len(r);
+    int page = -1, page_j = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e;
+      if (i >= tokens) break;
+      while (i >= cu[r + 1]) {
+        L = len(++r);
+        page_j = -1;
+      }
+      const int pos = L + (i - cu[r]);
+      const int j = pos >> p.p_shift, at = pos & ((1 << p.p_shift) - 1);
+      if (j != page_j) {
+        page_j = j;
+        const int have = pages_of(L, p.p_shift);
+        int* entry = p.table + static_cast<int64_t>(r) * p.max_pages + j;
+        if (j < have) {
+          page = *entry;
+        } else {
+          page = p.free_pages[top - (need[r] + (j - have))];
+          if (at == 0) *entry = page;
+        }
+      }
+      out[e] = (page << p.p_shift) + at;
+    }
+  }
+  if (i0 + 3 < p.tokens && (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0) {
+    *reinterpret_cast<int4*>(p.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i0 + e < p.tokens) p.slots[i0 + e] = out[e];
+  }
 }
 
-// One thread-block cluster does a whole step in one launch.  Every CTA sums
-// new tokens, new pages and returned pages over all sequences for itself (a
-// few KB from L2; cheaper than a second launch), pushes its share of the
-// returned pages, and after the cluster barrier, which also orders those
-// pushes and everybody's reads of the lengths before any write over them (the
-// outputs may be the inputs), takes its share of the slots.  The new page of
-// rank i in (sequence, page) order is entry free + returned - 1 - i of the
-// stack, so no thread depends on another one's pop.
-// Bound by latency: measured at 256 sequences and 256 tokens 1 CTA, at 2048
-// sequences and half a million tokens 8 CTAs.
+// One CTA: sums new tokens, new pages and returned pages over the sequences,
+// pushes the returned pages and writes the lengths.  The outputs may be the
+// inputs: everything is read before the barrier that the writes follow.  The new
+// page of rank i in (sequence, page) order is entry free + returned - 1 - i of
+// the stack, so no thread depends on another one's pop.  kSlots: the slots too
+// (few tokens: one launch); otherwise gla_cache_slots_kernel takes them.
+// Bound by latency: a handful of dependent trips to L2.
+template <bool kSlots>
 __global__ void __launch_bounds__(kPlanThreads, 1) gla_cache_plan_kernel(const PlanParams p) {
   extern __shared__ int plan_smem[];
-  __shared__ long long scratch[33];
+  __shared__ long long scratch[3][33];
   int* s_cu = plan_smem;              // [R + 1] new tokens
   int* s_need = s_cu + p.R + 1;       // [R + 1] new pages
   int* s_back = s_need + p.R + 1;     // [R + 1] returned pages
   int* s_len = s_back + p.R + 1;      // [R] cached tokens
   const int tid = threadIdx.x;
-  const int ctas = gridDim.x, cta = blockIdx.x;
 
   // sums over this thread's sequences, then over the block
   const int per = (p.R + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
-  long long tok = 0, need = 0, back = 0;
+  const long long free0 = *p.free_count;
+  long long sum[3] = {0, 0, 0}, all[3];  // new tokens, new pages, returned pages
   int wide = 0;
   for (int r = r0; r < r1; ++r) {
     const PlanSeq s = plan_seq(p, r);
-    tok += s.n;
-    need += s.np_new - s.np_old;
-    back += s.back();
+    sum[0] += s.n;
+    sum[1] += s.np_new - s.np_old;
+    sum[2] += s.back();
     wide |= s.np_new > p.max_pages;
   }
   const int too_wide = __syncthreads_or(wide);
-  long long tok_all, need_all, back_all;
-  tok = block_exclusive_scan<long long>(tok, scratch, tok_all);
-  need = block_exclusive_scan<long long>(need, scratch, need_all);
-  back = block_exclusive_scan<long long>(back, scratch, back_all);
-  const long long free0 = *p.free_count;
+  block_exclusive_scan_n<3, long long>(sum, scratch, all);
   int status = 0;
-  if (free0 + back_all < need_all) status |= 1;
-  if (tok_all > p.tokens) status |= 2;
+  if (free0 + all[2] < all[1]) status |= 1;
+  if (all[0] > p.tokens) status |= 2;
   if (too_wide) status |= 4;
-  if (free0 < 0 || free0 + back_all > p.pages) status |= 8;
+  if (free0 < 0 || free0 + all[2] > p.pages) status |= 8;
+  // what the sequences become: kept in registers over the barrier below
+  constexpr int kKeep = kCacheMaxSeqs / kPlanThreads;
+  int keep_len[kKeep], keep_held[kKeep];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int r = r0 + k;
+    if (r < r1) {
+      const PlanSeq s = plan_seq(p, r);
+      keep_len[k] = status ? p.lens[r] : (s.done ? 0 : s.L + s.n);
+      keep_held[k] = status ? p.held[r] : s.held_out;
+      if (status == 0) {
+        s_cu[r] = static_cast<int>(sum[0]);
+        s_need[r] = static_cast<int>(sum[1]);
+        s_back[r] = static_cast<int>(sum[2]);
+        s_len[r] = s.L;
+        sum[0] += s.n;
+        sum[1] += s.np_new - s.np_old;
+        sum[2] += s.back();
+      }
+    }
+  }
+  if (tid == 0 && status == 0) {
+    s_cu[p.R] = static_cast<int>(all[0]);
+    s_need[p.R] = static_cast<int>(all[1]);
+    s_back[p.R] = static_cast<int>(all[2]);
+  }
+  __syncthreads();
   if (status == 0) {
-    for (int r = r0; r < r1; ++r) {
+    for (int i = tid; i < static_cast<int>(all[2]); i += kPlanThreads) {
+      const int r = prefix_owner<int>(s_back, p.R, i);
       const PlanSeq s = plan_seq(p, r);
-      s_cu[r] = static_cast<int>(tok);
-      s_need[r] = static_cast<int>(need);
-      s_back[r] = static_cast<int>(back);
-      s_len[r] = static_cast<int>(s.L);
-      tok += s.n;
-      need += s.np_new - s.np_old;
-      back += s.back();
-    }
-    if (tid == 0) {
-      s_cu[p.R] = static_cast<int>(tok_all);
-      s_need[p.R] = static_cast<int>(need_all);
-      s_back[p.R] = static_cast<int>(back_all);
-    }
-    __syncthreads();
-    for (long long i = cta * kPlanThreads + tid; i < back_all; i += ctas * kPlanThreads) {
-      const int r = prefix_owner<int>(s_back, p.R, static_cast<int>(i));
-      const PlanSeq s = plan_seq(p, r);
-      const int64_t k = i - s_back[r];
-      const int64_t j = k < s.sink_back ? k : s.back_lo + (k - s.sink_back);
+      const int k = i - s_back[r];
+      const int j = k < s.sink_back ? k : s.back_lo + (k - s.sink_back);
       p.free_pages[free0 + i] = p.table[static_cast<int64_t>(r) * p.max_pages + j];
     }
   }
-  // the per-sequence outputs of this CTA's share, computed before the barrier
-  // (the inputs may be overwritten after it)
-  constexpr int kKeep = kCacheMaxSeqs / kPlanThreads;
-  int keep_len[kKeep], keep_held[kKeep];
-  if (cta == 0) {
+  __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k) {
-      const int r = tid + k * kPlanThreads;
-      if (r < p.R) {
-        const PlanSeq s = plan_seq(p, r);
-        keep_len[k] = status ? p.lens[r] : (s.done ? 0 : static_cast<int>(s.L + s.n));
-        keep_held[k] = status ? p.held[r] : static_cast<int>(s.held_out);
-      }
+  for (int k = 0; k < kKeep; ++k) {
+    const int r = r0 + k;
+    if (r < r1) {
+      p.lens_out[r] = keep_len[k];
+      p.held_out[r] = keep_held[k];
     }
   }
-  cluster_sync_all();
-  if (cta == 0) {
-#pragma unroll
-    for (int k = 0; k < kKeep; ++k) {
-      const int r = tid + k * kPlanThreads;
-      if (r < p.R) {
-        p.lens_out[r] = keep_len[k];
-        p.held_out[r] = keep_held[k];
-      }
-    }
-    for (int r = tid; r <= p.R; r += kPlanThreads) p.cu[r] = status ? 0 : s_cu[r];
-    if (tid == 0) {
-      *p.free_count_out = static_cast<int>(status ? free0 : free0 + back_all - need_all);
-      *p.status = status;
+  for (int r = tid; r <= p.R; r += kPlanThreads) p.cu[r] = status ? 0 : s_cu[r];
+  if (tid == 0) {
+    *p.free_count_out = static_cast<int>(status ? free0 : free0 + all[2] - all[1]);
+    *p.status = status;
+  }
+  if constexpr (kSlots) {
+    const int tokens = status ? 0 : static_cast<int>(all[0]);
+    const int top = static_cast<int>(free0 + all[2]) - 1;
+    for (int q = tid; q < (p.tokens + 3) >> 2; q += kPlanThreads)
+      plan_slots(p, q, tokens, s_cu, s_need, top, [&](int r) { return s_len[r]; });
+  }
+}
+
+// The slots of many tokens, over the whole GPU, from what the plan kernel wrote:
+// every CTA sums the new pages for itself (a few KB from L2).
+constexpr int kSlotThreads = 512;
+
+__global__ void __launch_bounds__(kSlotThreads) gla_cache_slots_kernel(const PlanParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ int slot_smem[];
+  __shared__ long long scratch[33];
+  int* s_cu = slot_smem;           // [R + 1]
+  int* s_need = s_cu + p.R + 1;    // [R + 1]
+  int* s_len = s_need + p.R + 1;   // [R]
+  const int tid = threadIdx.x;
+  const int status = *p.status;
+  const int per = (p.R + kSlotThreads - 1) / kSlotThreads;
+  const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
+  long long sum = 0, all;
+  if (status == 0) {
+    for (int r = r0; r < r1; ++r) {
+      const int c = p.cu[r], n = p.cu[r + 1] - c, L = p.lens_out[r] - n;
+      s_cu[r] = c;
+      s_len[r] = L;
+      s_need[r] = n > 0 ? pages_of(static_cast<int64_t>(L) + n, p.p_shift) - pages_of(L, p.p_shift)
+                        : 0;
+      sum += s_need[r];
     }
   }
-  // slots, four neighbouring tokens a thread: one search, then a walk
-  const long long top = free0 + back_all - 1;
-  const int quads = (p.tokens + 3) >> 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0;
-  for (int qd = cta * kPlanThreads + tid; qd < quads; qd += ctas * kPlanThreads) {
-    int out[4] = {-1, -1, -1, -1};
-    const int i0 = qd * 4;
-    if (status == 0 && i0 < tok_all) {
-      int r = prefix_owner<int>(s_cu, p.R, i0);
-      int64_t have = ceil_div64(s_len[r], p.P);
-      int page = -1;
-      int64_t page_j = -1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e;
-        if (i >= tok_all) break;
-        while (i >= s_cu[r + 1]) {
-          ++r;
-          have = ceil_div64(s_len[r], p.P);
-          page_j = -1;
-        }
-        const int64_t pos = static_cast<int64_t>(s_len[r]) + (i - s_cu[r]);
-        const int64_t j = pos / p.P;
-        if (j != page_j) {
-          page_j = j;
-          int* entry = p.table + static_cast<int64_t>(r) * p.max_pages + j;
-          if (j < have) {
-            page = *entry;
-          } else {
-            page = p.free_pages[top - (s_need[r] + (j - have))];
-            if (pos % p.P == 0) *entry = page;
-          }
-        }
-        out[e] = page * p.P + static_cast<int>(pos % p.P);
-      }
+  sum = block_exclusive_scan<long long>(sum, scratch, all);
+  int tokens = 0;
+  if (status == 0) {
+    for (int r = r0; r < r1; ++r) {
+      const int n = s_need[r];
+      s_need[r] = static_cast<int>(sum);
+      sum += n;
     }
-    if (vec && i0 + 3 < p.tokens) {
-      *reinterpret_cast<int4*>(p.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i0 + e < p.tokens) p.slots[i0 + e] = out[e];
-    }
+    tokens = p.cu[p.R];
+    if (tid == 0) s_cu[p.R] = tokens;
   }
+  __syncthreads();
+  const int top = *p.free_count_out + static_cast<int>(all) - 1;
+  for (int q = blockIdx.x * kSlotThreads + tid; q < (p.tokens + 3) >> 2;
+       q += gridDim.x * kSlotThreads)
+    plan_slots(p, q, tokens, s_cu, s_need, top, [&](int r) { return s_len[r]; });
 }
 
 // ------------------------------------------------------------------ store
@@ -307,65 +358,93 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // registers (the maximum needs all of them before the first code), coded and
 // written once.  Items are dealt out with the heads fastest, so that CTAs of
 // neighbouring items read whole token rows together.  128 threads keep P d / 8
-// / 128 16-byte loads each in flight and many CTAs share an SM.
+// / 128 16-byte loads each in flight and several CTAs share an SM; where the
+// next item lies is looked up while this one's loads are on their way.
 // Bound by HBM: 2 bytes in and 1 byte out for each value.
 template <int D, int P>
-__global__ void __launch_bounds__(kStoreThreads) gla_cache_store_kernel(const StoreParams p) {
-  constexpr int kRowChunks = D / 8;  // 16-byte chunks of a token row
-  constexpr int kRowsPerPass = kStoreThreads / kRowChunks;
-  constexpr int kPasses = P > kRowsPerPass ? P / kRowsPerPass : 1;
+struct StoreCfg {
+  static constexpr int kRowChunks = D / 8;  // 16-byte chunks of a token row
+  static constexpr int kRowsPerPass = kStoreThreads / kRowChunks;
+  static constexpr int kPasses = P / kRowsPerPass;
+  // CTAs of an SM: their loads together cover HBM's latency
+  static constexpr int kPerSm = kPasses >= 16 ? 4 : (kPasses >= 8 ? 6 : (kPasses >= 4 ? 8 : 12));
+};
+
+template <int D, int P>
+__global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
+    gla_cache_store_kernel(const StoreParams p) {
+  using C = StoreCfg<D, P>;
+  constexpr int kPasses = C::kPasses, kRowsPerPass = C::kRowsPerPass;
   extern __shared__ int s_items[];  // [R + 1] prefix sums of the pages each sequence writes
+  int* s_c0 = s_items + p.R + 1;    // [R + 1] first packed row of each sequence
+  int* s_old = s_c0 + p.R + 1;      // [R] tokens it held before
   __shared__ long long scratch[33];
   __shared__ uint32_t s_max[2][kStoreThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col = tid % kRowChunks, row0 = tid / kRowChunks;
-
-  auto seq = [&](int r, int& c0, int& n, int& old) {
-    c0 = min(max(p.cu[r], 0), p.tokens);
-    n = max(min(p.cu[r + 1], p.tokens) - c0, 0);
-    old = max(p.lens[r] - n, 0);
-  };
+  const int col = tid % C::kRowChunks, row0 = tid / C::kRowChunks;
   {
     const int per = (p.R + kStoreThreads - 1) / kStoreThreads;
     const int r0 = min(p.R, tid * per), r1 = min(p.R, r0 + per);
     long long sum = 0, all;
     for (int r = r0; r < r1; ++r) {
-      int c0, n, old;
-      seq(r, c0, n, old);
-      sum += n > 0 ? (static_cast<int64_t>(old) + n + P - 1) / P - old / P : 0;
+      const int c0 = min(max(p.cu[r], 0), p.tokens);
+      const int n = max(min(p.cu[r + 1], p.tokens) - c0, 0);
+      const int old = max(p.lens[r] - n, 0);
+      s_c0[r] = c0;
+      s_old[r] = old;
+      s_items[r] = n > 0 ? static_cast<int>((static_cast<int64_t>(old) + n + P - 1) / P - old / P)
+                         : 0;
+      sum += s_items[r];
     }
+    if (r1 == p.R && r0 < p.R) s_c0[p.R] = min(max(p.cu[p.R], 0), p.tokens);
     sum = block_exclusive_scan<long long>(sum, scratch, all);
     for (int r = r0; r < r1; ++r) {
-      int c0, n, old;
-      seq(r, c0, n, old);
+      const int n = s_items[r];
       s_items[r] = static_cast<int>(sum);
-      sum += n > 0 ? (static_cast<int64_t>(old) + n + P - 1) / P - old / P : 0;
+      sum += n;
     }
     if (tid == 0) s_items[p.R] = static_cast<int>(all);
     __syncthreads();
   }
-  const int64_t items = static_cast<int64_t>(s_items[p.R]) * p.H * 2;
+  // an item: its first token, its rows, the head and tensor, and the slot of
+  // its first token (the load is left in flight)
+  struct Item {
+    int t0, m, h, slot;
+    bool is_v;
+  };
+  const unsigned heads2 = 2u * p.H;
+  auto locate = [&](int64_t it) {
+    Item x;
+    const int run = static_cast<int>(static_cast<uint64_t>(it) / heads2);
+    const int rest = static_cast<int>(it - static_cast<int64_t>(run) * heads2);
+    x.is_v = rest >= p.H;
+    x.h = x.is_v ? rest - p.H : rest;
+    const int r = prefix_owner<int>(s_items, p.R, run);
+    const int old = s_old[r], c0 = s_c0[r], n = max(s_c0[r + 1] - c0, 0);
+    const int j = old / P + (run - s_items[r]);  // page of the sequence
+    const int64_t p0 = max(static_cast<int64_t>(j) * P, static_cast<int64_t>(old));
+    x.t0 = c0 + static_cast<int>(p0 - old);
+    x.m = static_cast<int>(
+        min(static_cast<int64_t>(j + 1) * P, static_cast<int64_t>(old) + n) - p0);
+    x.slot = __ldg(p.slots + x.t0);
+    return x;
+  };
+  const int64_t items = static_cast<int64_t>(s_items[p.R]) * heads2;
   int bad = 0;
   int flip = 0;
+  Item next{};
+  if (blockIdx.x < items) next = locate(blockIdx.x);
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x, flip ^= 1) {
-    const int64_t run = it / (2 * p.H);
-    const int rest = static_cast<int>(it - run * (2 * p.H));
-    const bool is_v = rest >= p.H;
-    const int h = is_v ? rest - p.H : rest;
-    const int r = prefix_owner<int>(s_items, p.R, static_cast<int>(run));
-    int c0, n, old;
-    seq(r, c0, n, old);
-    const int j = old / P + static_cast<int>(run - s_items[r]);  // page of the sequence
-    const int64_t p0 = max(static_cast<int64_t>(j) * P, static_cast<int64_t>(old));
-    const int t0 = c0 + static_cast<int>(p0 - old);
-    const int slot = p.slots[t0];
-    const int page = slot >= 0 ? slot / P : p.pages;
-    const int at = slot >= 0 ? slot % P : 0;
-    int m = static_cast<int>(min(static_cast<int64_t>(j + 1) * P, static_cast<int64_t>(old) + n) - p0);
-    m = page < p.pages ? min(m, P - at) : 0;  // a slot outside the cache: nothing to write
+    const Item cur = next;
+    const bool is_v = cur.is_v;
+    const int h = cur.h;
+    const int page = cur.slot >= 0 ? cur.slot / P : p.pages;
+    const int at = cur.slot >= 0 ? cur.slot % P : 0;
+    // a slot outside the cache: nothing to write
+    const int m = page < p.pages ? min(cur.m, P - at) : 0;
 
     const __nv_bfloat16* src =
-        (is_v ? p.v : p.k) + (static_cast<int64_t>(t0) * p.H + h) * D + col * 8;
+        (is_v ? p.v : p.k) + (static_cast<int64_t>(cur.t0) * p.H + h) * D + col * 8;
     uint4 x[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -374,6 +453,10 @@ __global__ void __launch_bounds__(kStoreThreads) gla_cache_store_kernel(const St
       if (row < m)
         x[i] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(row) * p.H * D));
     }
+    if (it + gridDim.x < items) next = locate(it + gridDim.x);
+    const int64_t blk = static_cast<int64_t>(m > 0 ? page : 0) * p.H + h;
+    float* scale_p = (is_v ? p.vs : p.ks) + blk;
+    const float was = at > 0 && m > 0 ? *scale_p : 0.f;
     // largest finite magnitude (packed 16-bit maxima of the bf16 bits); NaN
     // becomes 0, infinities stay for the saturating conversion
     uint32_t mx = 0;
@@ -397,15 +480,9 @@ __global__ void __launch_bounds__(kStoreThreads) gla_cache_store_kernel(const St
     __syncthreads();  // the other half of s_max is free again after this barrier
     mx = max(max(s_max[flip][0], s_max[flip][1]), max(s_max[flip][2], s_max[flip][3]));
     if (m <= 0) continue;  // uniform over the block
-    const int64_t blk = static_cast<int64_t>(page) * p.H + h;
-    float* scale_p = (is_v ? p.vs : p.ks) + blk;
     uint8_t* dst = (is_v ? p.v8 : p.k8) + blk * (P * D);
     float scale = exp2_int(scale_exponent(mx));
-    float was = 0.f;
-    if (at > 0) {
-      was = *scale_p;
-      scale = fmaxf(scale, was);
-    }
+    if (at > 0) scale = fmaxf(scale, was);
     const float inv = 1.0f / scale;  // exact: a power of two unless `was` is not one
     const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
 #pragma unroll
