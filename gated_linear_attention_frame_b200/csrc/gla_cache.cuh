@@ -457,24 +457,31 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
     const int64_t blk = static_cast<int64_t>(m > 0 ? page : 0) * p.H + h;
     float* scale_p = (is_v ? p.vs : p.ks) + blk;
     const float was = at > 0 && m > 0 ? *scale_p : 0.f;
-    // largest finite magnitude (packed 16-bit maxima of the bf16 bits); NaN
-    // becomes 0, infinities stay for the saturating conversion
+    // largest magnitude (packed 16-bit maxima of the bf16 bits)
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = w[e] & 0x7FFF7FFFu;
-        const uint32_t odd = __vcmpgeu2(a, 0x7F807F80u);  // 0xFFFF where not finite
-        if (odd) {
-          bad += __popc(odd) >> 4;
-          w[e] &= ~__vcmpgtu2(a, 0x7F807F80u);
-        }
-        mx = __vmaxu2(mx, a & ~odd);
-      }
+      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
     }
     mx = max(mx & 0xFFFFu, mx >> 16);
+    if (mx >= 0x7F80u) {
+      // some are not finite: they do not count for the scale; NaN becomes 0,
+      // infinities stay for the saturating conversion
+      mx = 0;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
+          bad += (lo >= 0x7F80u) + (hi >= 0x7F80u);
+          if (lo > 0x7F80u) w[e] &= 0xFFFF0000u;
+          if (hi > 0x7F80u) w[e] &= 0x0000FFFFu;
+          mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        }
+      }
+    }
     mx = __reduce_max_sync(0xffffffffu, mx);
     if (lane == 0) s_max[flip][warp] = mx;
     __syncthreads();  // the other half of s_max is free again after this barrier
@@ -483,8 +490,8 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
     uint8_t* dst = (is_v ? p.v8 : p.k8) + blk * (P * D);
     float scale = exp2_int(scale_exponent(mx));
     if (at > 0) scale = fmaxf(scale, was);
-    const float inv = 1.0f / scale;  // exact: a power of two unless `was` is not one
-    const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+    // both powers of two: the products below are exact in bf16
+    const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int row = row0 + i * kRowsPerPass;
@@ -492,8 +499,9 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
       uint32_t c[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float lo = bf16lo_to_f32(w[e]), hi = bf16hi_to_f32(w[e]);
-        c[e] = exact ? pack_e4m3x2(lo * inv, hi * inv) : pack_e4m3x2(lo / scale, hi / scale);
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), inv);
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
+        c[e] = pack_e4m3x2(bf16lo_to_f32(v), bf16hi_to_f32(v));
       }
       if (row < m)
         *reinterpret_cast<uint2*>(dst + (at + row) * D + col * 8) =
