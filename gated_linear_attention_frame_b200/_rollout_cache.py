@@ -27,53 +27,57 @@ _I32, _F32, _BF16, _FP8, _U8 = (torch.int32, torch.float32, torch.bfloat16, torc
                                 torch.uint8)
 
 
-class _Call:
-    """Checks of one call's tensors: kind, layout, size and one common device."""
+_BF, _CODE, _INT, _FLT = (_BF16,), (_FP8, _U8), (_I32,), (_F32,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    __slots__ = ("where", "device")
 
-    def __init__(self, where: str):
-        self.where = where
-        self.device = None
-
-    def __call__(self, name, x, dtypes, count):
-        """Device pointer of `x` (None -> NULL), which must hold at least
-        `count` elements of one of `dtypes`."""
-        if x is None:
-            return None
-        if isinstance(x, int):
-            return x
+def _pointers(where, specs):
+    """Device pointers of (name, tensor, dtypes, least element count) tuples and
+    the one device they are on (None: no tensor among them).  None -> NULL, an
+    int is taken as an address.  One loop, few calls: at the smallest sizes
+    this is most of a call's time."""
+    device = None
+    out = []
+    for name, x, dtypes, count in specs:
+        if x is None or type(x) is int:
+            out.append(x)
+            continue
         if not isinstance(x, torch.Tensor):
             raise TypeError("%s: %s must be a torch.Tensor, an int address or None, got %r"
-                            % (self.where, name, type(x)))
+                            % (where, name, type(x)))
         if x.dtype not in dtypes:
             raise TypeError("%s: %s must be %s, got %s"
-                            % (self.where, name, " or ".join(str(d) for d in dtypes), x.dtype))
-        if not x.is_cuda:
-            raise ValueError("%s: %s must be on a CUDA device (got %s)"
-                             % (self.where, name, x.device))
+                            % (where, name, " or ".join(str(d) for d in dtypes), x.dtype))
+        i = x.get_device()
+        if i != device:
+            if i < 0:
+                raise ValueError("%s: %s must be on a CUDA device (got %s)"
+                                 % (where, name, x.device))
+            if device is not None:
+                raise ValueError("%s: %s is on cuda:%d, other tensors are on cuda:%d"
+                                 % (where, name, i, device))
+            device = i
         if not x.is_contiguous():
-            raise ValueError("%s: %s must be contiguous" % (self.where, name))
+            raise ValueError("%s: %s must be contiguous" % (where, name))
         if x.numel() < count:
             raise ValueError("%s: %s holds %d elements, the sizes ask for %d"
-                             % (self.where, name, x.numel(), count))
-        i = x.get_device()
-        if self.device is None:
-            self.device = i
-        elif self.device != i:
-            raise ValueError("%s: %s is on cuda:%d, other tensors are on cuda:%d"
-                             % (self.where, name, i, self.device))
-        return x.data_ptr() or None
+                             % (where, name, x.numel(), count))
+        out.append(x.data_ptr() or None)
+    return out, device
 
-    def run(self, fn, args, stream):
-        """fn(*args, stream) on the tensors' device; a nonzero status raises."""
-        if self.device is None or self.device == torch.cuda.current_device():
-            st = fn(*args, _b._stream(stream))
-        else:
-            with torch.cuda.device(self.device):
-                st = fn(*args, _b._stream(stream))
-        if st != _b.GLA_OK:
-            raise _b.GLAError(st, self.where)
+
+def _run(where, fn, pointers, device, sizes, stream):
+    """fn(*pointers, *sizes, stream) on the tensors' device; a nonzero status
+    raises.  stream None: that device's current stream."""
+    if device is None or device == torch.cuda.current_device():
+        if stream is None and device is not None and _raw_stream is not None:
+            stream = _raw_stream(device)
+        st = fn(*pointers, *sizes, _b._stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*pointers, *sizes, _b._stream(stream))
+    if st != _b.GLA_OK:
+        raise _b.GLAError(st, where)
 
 
 def gla_cache_plan(lens, held, new_lens, free_count, free_pages, block_table, lens_out, held_out,
@@ -82,47 +86,46 @@ def gla_cache_plan(lens, held, new_lens, free_count, free_pages, block_table, le
     """Lengths, pages and slots of one step (see include/gla.h).  All arrays
     int32; raises GLAError on a nonzero return code.  Whether the step was
     admitted is in status[0] on the GPU."""
-    c = _Call("gla_cache_plan")
-    i = (_I32,)
-    args = (c("lens", lens, i, R), c("held", held, i, R), c("new_lens", new_lens, i, R),
-            c("free_count", free_count, i, 1), c("free_pages", free_pages, i, pages),
-            c("block_table", block_table, i, R * max_pages), c("lens_out", lens_out, i, R),
-            c("held_out", held_out, i, R), c("free_count_out", free_count_out, i, 1),
-            c("cu_tokens", cu_tokens, i, R + 1), c("slots", slots, i, tokens),
-            c("status", status, i, 1), R, max_pages, pages, page_tokens, tokens, frame_tokens,
-            window_frames, n_sink)
-    c.run(_b.load_library().gla_cache_plan, args, stream)
+    ptr, dev = _pointers("gla_cache_plan", (
+        ("lens", lens, _INT, R), ("held", held, _INT, R), ("new_lens", new_lens, _INT, R),
+        ("free_count", free_count, _INT, 1), ("free_pages", free_pages, _INT, pages),
+        ("block_table", block_table, _INT, R * max_pages), ("lens_out", lens_out, _INT, R),
+        ("held_out", held_out, _INT, R), ("free_count_out", free_count_out, _INT, 1),
+        ("cu_tokens", cu_tokens, _INT, R + 1), ("slots", slots, _INT, tokens),
+        ("status", status, _INT, 1)))
+    _run("gla_cache_plan", _b.load_library().gla_cache_plan, ptr, dev,
+         (R, max_pages, pages, page_tokens, tokens, frame_tokens, window_frames, n_sink), stream)
 
 
 def gla_cache_store(k, v, lens, cu_tokens, slots, k_cache, v_cache, k_scale, v_scale, nonfinite,
                     R, tokens, Hkv, d, pages, page_tokens, stream=None) -> None:
     """Quantise the new tokens' keys and values into the cache (see
     include/gla.h).  `nonfinite`: int32 counter tensor or None."""
-    c = _Call("gla_cache_store")
-    i, new, code = (_I32,), tokens * Hkv * d, pages * Hkv * page_tokens * d
-    args = (c("k", k, (_BF16,), new), c("v", v, (_BF16,), new), c("lens", lens, i, R),
-            c("cu_tokens", cu_tokens, i, R + 1), c("slots", slots, i, tokens),
-            c("k_cache", k_cache, (_FP8, _U8), code), c("v_cache", v_cache, (_FP8, _U8), code),
-            c("k_scale", k_scale, (_F32,), pages * Hkv),
-            c("v_scale", v_scale, (_F32,), pages * Hkv), c("nonfinite", nonfinite, i, 1), R,
-            tokens, Hkv, d, pages, page_tokens)
-    c.run(_b.load_library().gla_cache_store, args, stream)
+    new, code, blocks = tokens * Hkv * d, pages * Hkv * page_tokens * d, pages * Hkv
+    ptr, dev = _pointers("gla_cache_store", (
+        ("k", k, _BF, new), ("v", v, _BF, new), ("lens", lens, _INT, R),
+        ("cu_tokens", cu_tokens, _INT, R + 1), ("slots", slots, _INT, tokens),
+        ("k_cache", k_cache, _CODE, code), ("v_cache", v_cache, _CODE, code),
+        ("k_scale", k_scale, _FLT, blocks), ("v_scale", v_scale, _FLT, blocks),
+        ("nonfinite", nonfinite, _INT, 1)))
+    _run("gla_cache_store", _b.load_library().gla_cache_store, ptr, dev,
+         (R, tokens, Hkv, d, pages, page_tokens), stream)
 
 
 def gla_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_tokens,
                         gate_z, out, R, tokens, max_new, H, Hkv, d, pages, page_tokens, max_pages,
                         frame_tokens, window_frames, n_sink, scale, stream=None) -> None:
     """Attention of the new tokens over the cache (see include/gla.h)."""
-    c = _Call("gla_cache_attention")
-    i, new, code = (_I32,), tokens * H * d, pages * Hkv * page_tokens * d
-    args = (c("q", q, (_BF16,), new), c("k_cache", k_cache, (_FP8, _U8), code),
-            c("v_cache", v_cache, (_FP8, _U8), code), c("k_scale", k_scale, (_F32,), pages * Hkv),
-            c("v_scale", v_scale, (_F32,), pages * Hkv),
-            c("block_table", block_table, i, R * max_pages), c("lens", lens, i, R),
-            c("cu_tokens", cu_tokens, i, R + 1), c("gate_z", gate_z, (_BF16,), new),
-            c("out", out, (_BF16,), new), R, tokens, max_new, H, Hkv, d, pages, page_tokens,
-            max_pages, frame_tokens, window_frames, n_sink, scale)
-    c.run(_b.load_library().gla_cache_attention, args, stream)
+    new, code, blocks = tokens * H * d, pages * Hkv * page_tokens * d, pages * Hkv
+    ptr, dev = _pointers("gla_cache_attention", (
+        ("q", q, _BF, new), ("k_cache", k_cache, _CODE, code), ("v_cache", v_cache, _CODE, code),
+        ("k_scale", k_scale, _FLT, blocks), ("v_scale", v_scale, _FLT, blocks),
+        ("block_table", block_table, _INT, R * max_pages), ("lens", lens, _INT, R),
+        ("cu_tokens", cu_tokens, _INT, R + 1), ("gate_z", gate_z, _BF, new),
+        ("out", out, _BF, new)))
+    _run("gla_cache_attention", _b.load_library().gla_cache_attention, ptr, dev,
+         (R, tokens, max_new, H, Hkv, d, pages, page_tokens, max_pages, frame_tokens,
+          window_frames, n_sink, scale), stream)
 
 
 @dataclass

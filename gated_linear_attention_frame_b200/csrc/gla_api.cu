@@ -215,13 +215,16 @@ cudaError_t set_cache_attrs() {
     if (e != cudaSuccess) return e;
   }
   constexpr int kPre = (gla::kCacheMaxSeqs + 1) * 8;
-  e = cudaFuncSetAttribute(gla::gla_cache_token_kernel<64>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           gla::TokenCfg<64>::kFixedBytes + kPre);
+  auto token = [](auto* fn, int fixed) {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + kPre);
+  };
+  e = token(gla::gla_cache_token_kernel<64, 8>, gla::TokenCfg<64, 8>::kFixedBytes);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(gla::gla_cache_token_kernel<128>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           gla::TokenCfg<128>::kFixedBytes + kPre);
+  e = token(gla::gla_cache_token_kernel<64, 16>, gla::TokenCfg<64, 16>::kFixedBytes);
+  if (e != cudaSuccess) return e;
+  e = token(gla::gla_cache_token_kernel<128, 8>, gla::TokenCfg<128, 8>::kFixedBytes);
+  if (e != cudaSuccess) return e;
+  e = token(gla::gla_cache_token_kernel<128, 16>, gla::TokenCfg<128, 16>::kFixedBytes);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(gla::gla_cache_frame_kernel<64>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1101,10 +1104,10 @@ int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t strea
 // workspace.
 constexpr size_t kScheduleSmem = 160 * 1024;
 
-template <int D>
+template <int D, int R>
 int launch_combine(const gla::CacheAttnParams& p, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, gla::TokenCfg<D>::kRows);
+  cfg.gridDim = dim3(ctas, R);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1112,16 +1115,19 @@ int launch_combine(const gla::CacheAttnParams& p, int ctas, cudaStream_t stream)
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D>, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, gla::gla_cache_combine_kernel<D, R>, p) != cudaSuccess) {
     cudaGetLastError();
     return GLA_ERR_LAUNCH;
   }
   return GLA_OK;
 }
 
-template <int D>
+// R: query rows of a tile.
+template <int D, int R>
 int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t stream) {
-  using C = gla::TokenCfg<D>;
+  using C = gla::TokenCfg<D, R>;
+  p.tile_t = p.G <= R ? R / p.G : 1;
+  p.tile_c = p.G <= R ? 1 : (p.G + R - 1) / R;
   const int grid = di.sms * C::kCtasPerSm;
   const int64_t desc_bytes = align256(static_cast<int64_t>(grid) * 32);
   const int64_t part_bytes = static_cast<int64_t>(grid) * 2 * C::kPartFloats * 4;
@@ -1131,10 +1137,10 @@ int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
   p.desc = reinterpret_cast<int*>(ws);
   p.part = reinterpret_cast<float*>(ws + desc_bytes);
   const size_t smem = C::kFixedBytes + (static_cast<size_t>(p.R) + 1) * 8;
-  gla::gla_cache_token_kernel<D><<<grid, C::kThreads, smem, stream>>>(p);
+  gla::gla_cache_token_kernel<D, R><<<grid, C::kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) status = GLA_ERR_LAUNCH;
   if (status == GLA_OK) {
-    status = launch_combine<D>(p, grid, stream);
+    status = launch_combine<D, R>(p, grid, stream);
   }
   if (cudaFreeAsync(ws, stream) != cudaSuccess) {
     cudaGetLastError();
@@ -1229,13 +1235,15 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;
-  p.tile_t = p.G <= 16 ? 16 / p.G : 1;
-  p.tile_c = p.G <= 16 ? 1 : (p.G + 15) / 16;
   // up to 64 query rows of a sequence and head: the keys are read (row tiles)
-  // times; more fill the 128-row tiles of the tensor cores.  (The token
-  // kernel's tile numbers are 32-bit.)
-  if (static_cast<int64_t>(max_new) * p.G <= 64 && p.tokens <= (1 << 27))
-    return d == 64 ? run_cache_token<64>(p, di, stream) : run_cache_token<128>(p, di, stream);
+  // times, in one tile of 8 rows where they fit; more rows fill the 128-row
+  // tiles of the tensor cores.  (The token kernel's tile numbers are 32-bit.)
+  const int64_t rows = static_cast<int64_t>(max_new) * p.G;
+  if (rows <= 8 && p.tokens <= (1 << 26))
+    return d == 64 ? run_cache_token<64, 8>(p, di, stream) : run_cache_token<128, 8>(p, di, stream);
+  if (rows <= 64 && p.tokens <= (1 << 26))
+    return d == 64 ? run_cache_token<64, 16>(p, di, stream)
+                   : run_cache_token<128, 16>(p, di, stream);
   return d == 64 ? run_cache_frame<64>(p, di, stream) : run_cache_frame<128>(p, di, stream);
 }
 

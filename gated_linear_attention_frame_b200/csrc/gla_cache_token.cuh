@@ -175,28 +175,59 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// R: query rows of a tile, 16 or 8.  Rows of 16 are the M side of the products,
+// rows of 8 the N side (S^T = K Q^T, O^T = V^T P^T): half the products, half
+// the exponentials and half the accumulators, so that 12 warps fit on an SM
+// instead of 8.
+template <int D, int R>
 struct TokenCfg {
+  static_assert(R == 16 || R == 8, "rows of a tile");
   static constexpr int kThreads = 128;
   static constexpr int kWarps = 4;
-  static constexpr int kRows = 16;
+  static constexpr int kRows = R;
   static constexpr int BK = 32;           // keys of a block
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStages = D == 64 ? 4 : (R == 16 ? 3 : 2);
   static constexpr int kTensorBytes = BK * D;            // K or V codes of a block
   static constexpr int kStageBytes = 2 * kTensorBytes + 16;  // + ks, vs of its two key halves
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kMergeBytes = 2 * 8 * D * 4;  // two warps' rows, eight at a time
-  static constexpr int kStatBytes = kWarps * kRows * 8;
+  static constexpr int kStatBytes = kWarps * 16 * 8;
   static constexpr int kFixedBytes = kRingBytes + kMergeBytes + kStatBytes;
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
-  static constexpr int kCtasPerSm = 2;
+  static constexpr int kCtasPerSm = R == 16 ? 2 : 3;
   static constexpr int kMinBlocks = 8;    // least blocks of a CTA
   static constexpr int kChunks = D / 16;  // 16-byte chunks of a key
 };
 
-template <int D>
-__global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttnParams p) {
-  using C = TokenCfg<D>;
+// The same, A by value.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  const uint32_t a[4] = {a0, a1, a2, a3};
+  mma_f16_16816(d, a, b0, b1);
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values held as a fragment (lane 4 r + c:
+// row r, columns 2 c and 2 c + 1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+// Four codes of two neighbouring keys (a, b) -> their fp16 pairs (key a in the
+// low half), code by code.
+__device__ __forceinline__ void pair_keys(uint32_t a, uint32_t b, uint32_t (&y)[4]) {
+  const uint32_t lo = __byte_perm(a, b, 0x5140), hi = __byte_perm(a, b, 0x7362);
+  y[0] = e4m3x2_to_f16x2(lo & 0xFFFFu);
+  y[1] = e4m3x2_to_f16x2(lo >> 16);
+  y[2] = e4m3x2_to_f16x2(hi & 0xFFFFu);
+  y[3] = e4m3x2_to_f16x2(hi >> 16);
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
+    gla_cache_token_kernel(const CacheAttnParams p) {
+  using C = TokenCfg<D, R>;
   constexpr int BK = C::BK;
   constexpr int KI = D / 64;   // 16-byte chunks of a key that one thread reads
   constexpr int NT = D / 8;    // n-tiles of the output
@@ -315,6 +346,13 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
   const int64_t page_stride = static_cast<int64_t>(p.Hkv) << p.p_shift;  // rows of a page
 
+  constexpr int kRowsPerPass = 32 / C::kChunks;  // 4 (d = 128) or 8
+  const int ch = lane % C::kChunks, rr = lane / C::kChunks;
+  // where this lane's chunk goes in a stage: swizzled so that the fragment
+  // reads below hit all banks (V: every other pass flips one more bit at d = 128)
+  const uint32_t to_k = rr * D + (D == 128 ? (ch ^ ((rr & 1) << 2)) : ch) * 16;
+  const uint32_t to_v = rr * D + (D == 128 ? (ch ^ ((rr >> 1) << 1)) : (ch ^ ((rr >> 1) & 3))) * 16;
+
   // Start the copies of this warp's next block into stage `st`.
   auto issue = [&](int st) {
     while (ld.live && ld.k >= ld.k_end) next_unit(ld);
@@ -322,33 +360,33 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       const int base = ld.v.pos(ld.k, BK);
       const int* row = p.table + static_cast<int64_t>(ld.r) * p.max_pages;
       const uint32_t dst = ring + st * C::kStageBytes;
-      constexpr int kRowsPerPass = 32 / C::kChunks;  // 4 (d = 128) or 8
-      const int ch = lane % C::kChunks, rr = lane / C::kChunks;
       // a block lies in one page, or (P = 16) each half of it in one
+      const int j0 = base >> p.p_shift, j1 = (base + 16) >> p.p_shift;
       int page[2];
+      page[0] = j0 < p.max_pages ? row[j0] : -1;
+      page[1] = j1 == j0 ? page[0] : (j1 < p.max_pages ? row[j1] : -1);
+      const uint8_t *ks[2], *vs[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int key = base + hf * 16;
-        const int j = key >> p.p_shift;
-        int pg = j < p.max_pages ? row[j] : -1;
-        if (pg >= p.pages) pg = -1;
-        page[hf] = pg;
+        if (page[hf] >= p.pages) page[hf] = -1;
+        const int64_t off = (max(page[hf], 0) * page_stride +
+                             (static_cast<int64_t>(ld.h) << p.p_shift) +
+                             ((base + hf * 16 + rr) & (P - 1))) * D + ch * 16;
+        ks[hf] = p.k8 + off;
+        vs[hf] = p.v8 + off;
       }
+      const bool all = base >= ld.v.lo && base + BK <= ld.v.hi && page[0] >= 0 && page[1] >= 0;
 #pragma unroll
       for (int i = 0; i < BK / kRowsPerPass; ++i) {
-        const int kr = i * kRowsPerPass + rr;  // key of the block
-        const int key = base + kr;
-        const int pg = page[kr >> 4];
-        const bool ok = pg >= 0 && ld.v.sees(key);
-        const int64_t off =
-            ok ? (pg * page_stride + (static_cast<int64_t>(ld.h) << p.p_shift) + (key & (P - 1))) *
-                         D + ch * 16
-               : 0;
-        // 16-byte chunks swizzled so that the fragment reads below hit all banks
-        const int ck = D == 128 ? (ch ^ ((kr & 1) << 2)) : ch;
-        const int cv = D == 128 ? (ch ^ (((kr >> 1) & 3) << 1)) : (ch ^ ((kr >> 1) & 3));
-        cp_async16(dst + kr * D + ck * 16, p.k8 + off, ok);
-        cp_async16(dst + C::kTensorBytes + kr * D + cv * 16, p.v8 + off, ok);
+        constexpr int kHalf = 16 / kRowsPerPass;  // passes of one half
+        const int hf = i / kHalf;
+        const bool ok =
+            all || (page[hf] >= 0 && ld.v.sees(base + i * kRowsPerPass + rr));
+        const int step = (i % kHalf) * kRowsPerPass * D;
+        cp_async16(dst + to_k + i * kRowsPerPass * D, ks[hf] + step, ok);
+        cp_async16(dst + C::kTensorBytes + (to_v ^ (D == 128 ? (i & 1) << 6 : 0)) +
+                       i * kRowsPerPass * D,
+                   vs[hf] + step, ok);
       }
       if (lane < 4) {
         const int hf = lane & 1;
@@ -362,31 +400,28 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
     }
     cp_async_commit();
   };
-#pragma unroll 1
-  for (int s = 0; s < C::kStages; ++s) issue(s);
-  int st = 0;
+  int ahead = 0;               // blocks in the ring
+  int st_in = 0, st = 0;       // stages filled and used next
 
   for (; cur.live; next_unit(cur)) {
     // rows of the tile: token t0 + row / G, head g0 + row % G of the group
     const int t0 = first_token(cur.tile);
-    const int g0 = p.tile_c > 1 ? (cur.tile - t0 * p.tile_c) * 16 : 0;
-    const int rows = p.tile_c > 1 ? min(16, p.G - g0) : min(p.tile_t, cur.s.n - t0) * p.G;
+    const int g0 = p.tile_c > 1 ? (cur.tile - t0 * p.tile_c) * R : 0;
+    const int rows = p.tile_c > 1 ? min(R, p.G - g0) : min(p.tile_t, cur.s.n - t0) * p.G;
     const int64_t row0 =
         (static_cast<int64_t>(cur.s.c0) + t0) * p.H + cur.h * p.G + g0;  // of q and out
     auto row_token = [&](int rho) { return p.tile_c > 1 ? 0 : small_div(rho, gm); };
-    // ---- query fragments: rows g and g + 8 of the tile
-    uint32_t qa[D / 16][4];
-    float rs[2];                 // undoes the row scale, times scale log2(e)
-    int hi[2], lo[2];
+    // ---- query fragments: rows g (and g + 8) of the tile
+    constexpr int E = R / 8;     // rows of a lane's fragment
+    uint32_t qa[D / 16][2 * E];
+    float rq[E];                 // undoes the row scale, times scale log2(e)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int rho = g + 8 * e;
       const bool have = rho < rows;
       const int rt = have ? row_token(rho) : 0;
       const __nv_bfloat16* qp =
           p.q + (row0 + static_cast<int64_t>(rt) * p.H + (have ? rho - rt * p.G : 0)) * D;
-      hi[e] = have ? key_hi(p, cur.s, cur.s.p0 + t0 + rt) : 0;
-      lo[e] = key_lo(p, cur.s.p0 + t0 + rt);
       uint4 w[KI][2];
       uint32_t mx = 0;
 #pragma unroll
@@ -404,7 +439,7 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int up = row_exponent(mx);
       const float f = exp2_int(up);
-      rs[e] = exp2_int(-up) * p.sl2;
+      rq[e] = exp2_int(-up) * p.sl2;
 #pragma unroll
       for (int i = 0; i < KI; ++i)
 #pragma unroll
@@ -412,39 +447,74 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
           const uint4& x = w[i][jj >> 1];
           const uint32_t w0 = (jj & 1) ? x.z : x.x, w1 = (jj & 1) ? x.w : x.y;
           qa[i * 4 + jj][e] = pack_f16x2(bf16lo_to_f32(w0) * f, bf16hi_to_f32(w0) * f);
-          qa[i * 4 + jj][2 + e] = pack_f16x2(bf16lo_to_f32(w1) * f, bf16hi_to_f32(w1) * f);
+          qa[i * 4 + jj][E + e] = pack_f16x2(bf16lo_to_f32(w1) * f, bf16hi_to_f32(w1) * f);
         }
     }
-    float o[NT][4];
+    // the rows of this lane's scores: g and g + 8, or (8 rows) 2 t4 and 2 t4 + 1
+    float rs[2];
+    int hi[2], lo[2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      const int rho = R == 16 ? g + 8 * e : 2 * t4 + e;
+      rs[e] = R == 16 ? rq[e % E] : __shfl_sync(0xffffffffu, rq[0], rho * 4);
+      const bool have = rho < rows;
+      const int pos = cur.s.p0 + t0 + (have ? row_token(rho) : 0);
+      hi[e] = have ? key_hi(p, cur.s, pos) : 0;
+      lo[e] = key_lo(p, pos);
+    }
+    // accumulators: 16 rows: n-tile n, [row g: x = 0, 1; row g + 8: x = 2, 3];
+    // 8 rows: m-tile n, [d 2 n of the lane's: rows 2 t4, 2 t4 + 1; d 2 n + 1: the same]
+    constexpr int NO = R == 16 ? NT : D / 16;
+    float o[NO][4];
+#pragma unroll
+    for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     // every row sees every key of a block inside [all_lo, all_hi)
     const int all_hi = key_hi(p, cur.s, cur.s.p0 + t0);
     const int all_lo = key_lo(p, cur.s.p0 + t0 + row_token(rows - 1));
 
-    for (; cur.k < cur.k_end; cur.k += C::kWarps) {
+    for (;; cur.k += C::kWarps) {
+#pragma unroll 1
+      for (; ahead < C::kStages; ++ahead) {  // all of them at first, then one a block
+        issue(st_in);
+        st_in = st_in + 1 == C::kStages ? 0 : st_in + 1;
+      }
+      if (cur.k >= cur.k_end) break;
       cp_async_wait<C::kStages - 1>();
       __syncwarp();
       const uint32_t kb = ring + st * C::kStageBytes, vb = kb + C::kTensorBytes;
       const uint4 sc = ld_shared_v4(vb + C::kTensorBytes);
       const float ksc[2] = {__uint_as_float(sc.x), __uint_as_float(sc.y)};
       const float vsc[2] = {__uint_as_float(sc.z), __uint_as_float(sc.w)};
-      // ---- S = Q K^T: 16 rows x 32 keys
-      float s[4][4];
+      // ---- S: 16 scores of 16 rows (n-tile j: keys 8 j ..), or 8 of 8 rows (m-tile
+      // j: keys 16 j ..) for each lane
+      constexpr int NS = R == 16 ? 4 : 2;
+      float s[NS][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NS; ++j) {
         s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        const int kr = j * 8 + g;
 #pragma unroll
         for (int i = 0; i < KI; ++i) {
           const int c = i * 4 + t4;
-          const uint4 w = ld_shared_v4(kb + kr * D + (D == 128 ? (c ^ ((kr & 1) << 2)) : c) * 16);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          auto chunk = [&](int kr) {
+            return ld_shared_v4(kb + kr * D + (D == 128 ? (c ^ ((kr & 1) << 2)) : c) * 16);
+          };
+          if constexpr (R == 16) {
+            const uint4 w = chunk(j * 8 + g);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int jj = 0; jj < 4; ++jj)
-            mma_f16_16816(s[j], qa[i * 4 + jj], e4m3x2_to_f16x2(ww[jj] & 0xFFFFu),
-                          e4m3x2_to_f16x2(ww[jj] >> 16));
+            for (int jj = 0; jj < 4; ++jj)
+              mma_f16_16816(s[j], qa[i * 4 + jj], e4m3x2_to_f16x2(ww[jj] & 0xFFFFu),
+                            e4m3x2_to_f16x2(ww[jj] >> 16));
+          } else {
+            const uint4 w = chunk(j * 16 + g), v = chunk(j * 16 + 8 + g);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+              mma_f16_16816(s[j], e4m3x2_to_f16x2(ww[jj] & 0xFFFFu),
+                            e4m3x2_to_f16x2(vv[jj] & 0xFFFFu), e4m3x2_to_f16x2(ww[jj] >> 16),
+                            e4m3x2_to_f16x2(vv[jj] >> 16), qa[i * 4 + jj][0], qa[i * 4 + jj][1]);
+          }
         }
       }
       const int base = cur.v.pos(cur.k, BK);
@@ -455,14 +525,18 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
         iv[hf] = vsc[hf] > 0.f ? ex2_approx(-lv[hf]) : 0.f;
       }
       const bool whole = base >= all_lo && base + BK <= all_hi;  // uniform
+      // score (j, x) belongs to row e = row_of(x), in key half half_of(j)
+      auto row_of = [](int x) { return R == 16 ? x >> 1 : x & 1; };
+      auto half_of = [](int j) { return R == 16 ? j >> 1 : j; };
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NS; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int e = x >> 1;
-          s[j][x] = fmaf(s[j][x], rs[e] * ksc[j >> 1], lv[j >> 1]);
+          const int e = row_of(x);
+          s[j][x] = fmaf(s[j][x], rs[e] * ksc[half_of(j)], lv[half_of(j)]);
           if (!whole) {
-            const int key = base + j * 8 + t4 * 2 + (x & 1);
+            const int key =
+                base + (R == 16 ? j * 8 + t4 * 2 + (x & 1) : j * 16 + g + (x >> 1) * 8);
             if (!(key < hi[e] && (key >= lo[e] || key < p.n_sink))) s[j][x] = -INFINITY;
           }
         }
@@ -472,116 +546,128 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       for (int e = 0; e < 2; ++e) {
         float a = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a = fmax3(a, s[j][2 * e], s[j][2 * e + 1]);
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        for (int j = 0; j < NS; ++j)
+          a = R == 16 ? fmax3(a, s[j][2 * e], s[j][2 * e + 1]) : fmax3(a, s[j][e], s[j][2 + e]);
+        if (R == 16) {  // over the lanes of a row
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        } else {
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16));
+        }
         mt[e] = a;
-        grow |= a > m[e] + kCacheLazy || (m[e] == -INFINITY && a != -INFINITY);
+        grow |= a > m[e] + kCacheLazy;  // also the first visible key: m = -inf
       }
       if (__any_sync(0xffffffffu, grow)) {
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float mn = fmaxf(m[e], mt[e]);
-          const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mn);
+          f[e] = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mn);
           m[e] = mn;
-          l[e] *= f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n][2 * e] *= f;
-            o[n][2 * e + 1] *= f;
-          }
+          l[e] *= f[e];
         }
+#pragma unroll
+        for (int n = 0; n < NO; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[n][x] *= f[row_of(x)];
       }
       // ---- P' and the row sums (the value scale leaves the sums again)
-      uint32_t pa[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float sh = m[e] == -INFINITY ? 0.f : kCacheBias - m[e];
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float x[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) x[y] = ex2_approx(s[hf * 2 + (y >> 1)][2 * e + (y & 1)] + sh);
-          l[e] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv[hf], l[e]);
-          pa[hf][e] = pack_f16x2(x[0], x[1]);
-          pa[hf][2 + e] = pack_f16x2(x[2], x[3]);
-        }
-      }
-      // ---- O += P' V
+      const float sh[2] = {m[0] == -INFINITY ? 0.f : kCacheBias - m[0],
+                           m[1] == -INFINITY ? 0.f : kCacheBias - m[1]};
+      uint32_t pa[2][4];  // 16 rows: A fragment of each key half; 8 rows: B fragment in [0], [1]
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        if constexpr (D == 128) {
-          uint4 w[4];
+        if constexpr (R == 16) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int kr = hf * 16 + t4 * 2 + (y & 1) + (y >> 1) * 8;
-            w[y] = ld_shared_v4(vb + kr * D + ((g ^ (((kr >> 1) & 3) << 1))) * 16);
-          }
+          for (int e = 0; e < 2; ++e) {
+            float x[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t a0 = (&w[0].x)[q], a1 = (&w[1].x)[q], a2 = (&w[2].x)[q],
-                           a3 = (&w[3].x)[q];
-            const uint32_t b0 = __byte_perm(a0, a1, 0x5140), b1 = __byte_perm(a2, a3, 0x5140);
-            const uint32_t c0 = __byte_perm(a0, a1, 0x7362), c1 = __byte_perm(a2, a3, 0x7362);
-            mma_f16_16816(o[q * 4 + 0], pa[hf], e4m3x2_to_f16x2(b0 & 0xFFFFu),
-                          e4m3x2_to_f16x2(b1 & 0xFFFFu));
-            mma_f16_16816(o[q * 4 + 1], pa[hf], e4m3x2_to_f16x2(b0 >> 16),
-                          e4m3x2_to_f16x2(b1 >> 16));
-            mma_f16_16816(o[q * 4 + 2], pa[hf], e4m3x2_to_f16x2(c0 & 0xFFFFu),
-                          e4m3x2_to_f16x2(c1 & 0xFFFFu));
-            mma_f16_16816(o[q * 4 + 3], pa[hf], e4m3x2_to_f16x2(c0 >> 16),
-                          e4m3x2_to_f16x2(c1 >> 16));
+            for (int y = 0; y < 4; ++y)
+              x[y] = ex2_approx(s[hf * 2 + (y >> 1)][2 * e + (y & 1)] + sh[e]);
+            l[e] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv[hf], l[e]);
+            pa[hf][e] = pack_f16x2(x[0], x[1]);
+            pa[hf][2 + e] = pack_f16x2(x[2], x[3]);
           }
         } else {
-          uint2 w[4];
+          float x[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int kr = hf * 16 + t4 * 2 + (y & 1) + (y >> 1) * 8;
+          for (int y = 0; y < 4; ++y) x[y] = ex2_approx(s[hf][y] + sh[y & 1]);
+          l[0] = fmaf(x[0] + x[2], iv[hf], l[0]);
+          l[1] = fmaf(x[1] + x[3], iv[hf], l[1]);
+          pa[hf][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));  // keys 0 .. 7 of the half
+          pa[hf][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));  // keys 8 .. 15
+        }
+      }
+      // ---- O += P' V.  Lane (g, t4) reads the bytes of d = D / 8 g .. of the keys
+      // 2 t4, 2 t4 + 1 and those plus 8
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        constexpr int NW = D / 32;  // words of a lane's piece of a key
+        uint32_t w[4][NW];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int kr = hf * 16 + t4 * 2 + (y & 1) + (y >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 v = ld_shared_v4(vb + kr * D + ((g ^ (((kr >> 1) & 3) << 1))) * 16);
+            w[y][0] = v.x;
+            w[y][1] = v.y;
+            w[y][2] = v.z;
+            w[y][3] = v.w;
+          } else {
             const uint32_t ad = vb + kr * D + (((g >> 1) ^ ((kr >> 1) & 3)) * 16) + (g & 1) * 8;
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(w[y].x), "=r"(w[y].y)
+                         : "=r"(w[y][0]), "=r"(w[y][1])
                          : "r"(ad)
                          : "memory");
           }
+        }
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t a0 = q ? w[0].y : w[0].x, a1 = q ? w[1].y : w[1].x,
-                           a2 = q ? w[2].y : w[2].x, a3 = q ? w[3].y : w[3].x;
-            const uint32_t b0 = __byte_perm(a0, a1, 0x5140), b1 = __byte_perm(a2, a3, 0x5140);
-            const uint32_t c0 = __byte_perm(a0, a1, 0x7362), c1 = __byte_perm(a2, a3, 0x7362);
-            mma_f16_16816(o[q * 4 + 0], pa[hf], e4m3x2_to_f16x2(b0 & 0xFFFFu),
-                          e4m3x2_to_f16x2(b1 & 0xFFFFu));
-            mma_f16_16816(o[q * 4 + 1], pa[hf], e4m3x2_to_f16x2(b0 >> 16),
-                          e4m3x2_to_f16x2(b1 >> 16));
-            mma_f16_16816(o[q * 4 + 2], pa[hf], e4m3x2_to_f16x2(c0 & 0xFFFFu),
-                          e4m3x2_to_f16x2(c1 & 0xFFFFu));
-            mma_f16_16816(o[q * 4 + 3], pa[hf], e4m3x2_to_f16x2(c0 >> 16),
-                          e4m3x2_to_f16x2(c1 >> 16));
+        for (int q = 0; q < NW; ++q) {
+          uint32_t a[4], b[4];  // codes 4 q .. 4 q + 3 of the piece: keys 2 t4 .., and plus 8
+          pair_keys(w[0][q], w[1][q], a);
+          pair_keys(w[2][q], w[3][q], b);
+          if constexpr (R == 16) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mma_f16_16816(o[q * 4 + y], pa[hf], a[y], b[y]);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              mma_f16_16816(o[q * 2 + y], a[2 * y], a[2 * y + 1], b[2 * y], b[2 * y + 1],
+                            pa[hf][0], pa[hf][1]);
           }
         }
       }
       __syncwarp();  // the stage is read by every lane before it is loaded again
-      issue(st);
       st = st + 1 == C::kStages ? 0 : st + 1;
+      --ahead;
     }
 
-    // ---- join the four warps.  Thread (g, t4) holds rows g, g + 8 and the
-    // columns D / 4 t4 .. + D / 4 - 1 (n-tile n: columns n and D / 8 + n of them).
+    // ---- join the four warps
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-      if (t4 == 0) s_ml[warp * 16 + g + 8 * e] = make_float2(m[e], l[e]);
+      if (R == 16) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        if (t4 == 0) s_ml[warp * 16 + g + 8 * e] = make_float2(m[e], l[e]);
+      } else {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+        if (g == 0) s_ml[warp * 16 + 2 * t4 + e] = make_float2(m[e], l[e]);
+      }
     }
     __syncthreads();
     float mm[2], ll[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+      const int rho = R == 16 ? g + 8 * e : 2 * t4 + e;
       float2 a[C::kWarps];
       mm[e] = -INFINITY;
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
-        a[w] = s_ml[w * 16 + g + 8 * e];
+        a[w] = s_ml[w * 16 + rho];
         mm[e] = fmaxf(mm[e], a[w].x);
       }
       ll[e] = 0.f;
@@ -590,21 +676,26 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
         ll[e] += a[w].x == -INFINITY ? 0.f : a[w].y * ex2_approx(a[w].x - mm[e]);
       const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mm[e]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][2 * e] *= f;
-        o[n][2 * e + 1] *= f;
-      }
+      for (int n = 0; n < NO; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if ((R == 16 ? x >> 1 : x & 1) == e) o[n][x] *= f;
     }
+    // eight rows at a time: 2 NT floats a lane
+    auto piece = [&](int e, int i) -> float& {
+      if constexpr (R == 16)
+        return o[i >> 1][2 * e + (i & 1)];
+      else
+        return o[i >> 2][i & 3];
+    };
     const bool low = rows > 8;  // rows g + 8 hold something (uniform)
     const bool starts = cur.k0 == 0, ends = cur.k_end == cur.v.nb, whole = starts && ends;
     // the CTA's first part of a unit begun before it goes to its partial 0, a
     // unit that goes on after it to partial 1
     float* part = p.part + (2ll * blockIdx.x + (starts ? 1 : 0)) * C::kPartFloats;
-    auto slot = [&](int buf, int n, int x) -> float& {
-      return s_o[((buf * 2 * NT) + n * 2 + x) * 32 + lane];
-    };
+    auto slot = [&](int buf, int i) -> float& { return s_o[(buf * 2 * NT + i) * 32 + lane]; };
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {  // rows g, then rows g + 8
+    for (int e = 0; e < R / 8; ++e) {  // rows g, then rows g + 8
       if (e == 1) {
         if (!low) break;
         __syncthreads();  // the buffers are read
@@ -614,30 +705,26 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
         if (warp >= half && warp < 2 * half) {
           const int buf = half == 2 ? warp - 2 : 1;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            slot(buf, n, 0) = o[n][2 * e];
-            slot(buf, n, 1) = o[n][2 * e + 1];
-          }
+          for (int i = 0; i < 2 * NT; ++i) slot(buf, i) = piece(e, i);
         }
         __syncthreads();
         if (warp < half) {
           const int buf = half == 2 ? warp : 1;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n][2 * e] += slot(buf, n, 0);
-            o[n][2 * e + 1] += slot(buf, n, 1);
-          }
+          for (int i = 0; i < 2 * NT; ++i) piece(e, i) += slot(buf, i);
         }
       }
       // warp 0 holds the sums: through shared memory once more, so that all
       // threads write whole row pieces of 8 columns
       if (warp == 0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          slot(0, n, 0) = o[n][2 * e];
-          slot(0, n, 1) = o[n][2 * e + 1];
+        for (int i = 0; i < 2 * NT; ++i) slot(0, i) = piece(e, i);
+        if (R == 16) {
+          if (t4 == 0) s_row[g] = make_float2(mm[e], ll[e]);
+        } else if (g == 0) {
+          s_row[2 * t4] = make_float2(mm[0], ll[0]);
+          s_row[2 * t4 + 1] = make_float2(mm[1], ll[1]);
         }
-        if (t4 == 0) s_row[g] = make_float2(mm[e], ll[e]);
       }
       __syncthreads();
       constexpr int kPieces = D / 8;  // of a row
@@ -645,12 +732,19 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
       for (int i = tid; i < 8 * kPieces; i += C::kThreads) {
         const int r8 = i / kPieces, c = i % kPieces, rho = r8 + 8 * e;
         if (rho >= rows) continue;
-        // columns 8 c .. 8 c + 7: thread (r8, col / (D / 4)), its n-tiles col % NT
-        // of half (col / NT) & 1
-        const int t = c * 8 / (D / 4), x = (c * 8 / NT) & 1, n0 = c * 8 % NT;
+        // column 8 c + y: with 16 rows lane (r8, col / (D / 4)) holds it in n-tile
+        // col % NT, x = (col / NT) & 1; with 8 rows lane (col / (D / 8), r8 / 2) in
+        // m-tile (col % (D / 8)) / 2, x = 2 (col & 1) + (r8 & 1)
         float v[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) v[y] = s_o[((n0 + y) * 2 + x) * 32 + r8 * 4 + t];
+        for (int y = 0; y < 8; ++y) {
+          const int col = c * 8 + y;
+          if constexpr (R == 16)
+            v[y] = s_o[((col % NT) * 2 + ((col / NT) & 1)) * 32 + r8 * 4 + col / (D / 4)];
+          else
+            v[y] = s_o[(((col % (D / 8)) >> 1) * 4 + (col & 1) * 2 + (r8 & 1)) * 32 +
+                       (col / (D / 8)) * 4 + (r8 >> 1)];
+        }
         const float2 ml = s_row[r8];
         if (whole) {
           const int rt = row_token(rho);
@@ -675,7 +769,7 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
           float4* dst = reinterpret_cast<float4*>(part + rho * D + c * 8);
           dst[0] = make_float4(v[0], v[1], v[2], v[3]);
           dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-          if (c == 0) *reinterpret_cast<float2*>(part + 16 * D + 2 * rho) = ml;
+          if (c == 0) *reinterpret_cast<float2*>(part + R * D + 2 * rho) = ml;
         }
       }
     }
@@ -698,11 +792,11 @@ __global__ void __launch_bounds__(128, 2) gla_cache_token_kernel(const CacheAttn
 // after it; its parts are partial 1 of that CTA and partial 0 of the next
 // ones.  blockIdx.y: a query row.  Four (eight at d = 64) groups of threads
 // take every fourth (eighth) part; the sums are joined in a fixed order.
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int kGroups = 128 / (D / 4);
-  constexpr int part_floats = TokenCfg<D>::kPartFloats, part_rows = TokenCfg<D>::kRows;
+  constexpr int part_floats = TokenCfg<D, R>::kPartFloats, part_rows = R;
   __shared__ float4 s_acc[128];
   __shared__ float s_m[kGroups], s_l[kGroups];
   const int* desc = p.desc + 8 * blockIdx.x;
