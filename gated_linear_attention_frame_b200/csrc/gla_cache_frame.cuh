@@ -233,6 +233,7 @@ constexpr int kJoinTiles = 6;  // what writing and joining partials costs, in ti
 struct FrameSchedule {
   int4* starts;
   int* n;
+  long long* meta;    // tiles, CTAs that share them
   long long* prefix;  // used when the entries do not fit in shared memory
   int entries_max;    // host bound of the entries (units of one kv head)
   int use_smem;
@@ -291,8 +292,6 @@ __global__ void __launch_bounds__(1024, 1)
     __syncthreads();
   }
   const long long tiles = total * p.Hkv;
-  const long long want = (tiles + FrameCfg<D>::kMinTiles - 1) / FrameCfg<D>::kMinTiles;
-  const int ctas = static_cast<int>(want < fs.ctas ? want : fs.ctas);
   // unit of tile x0 (order: sequence, kv head, unit) and the tile within it
   auto find = [&](long long x0, int& tiles_of_unit) {
     int lo = 0, hi = p.R;  // sequence: tiles before lo <= x0 < tiles before hi
@@ -315,24 +314,31 @@ __global__ void __launch_bounds__(1024, 1)
     tiles_of_unit = static_cast<int>(pre[e0[lo] + st.z + 1] - pre[e0[lo] + st.z]);
     return st;
   };
-  // Equal shares, cut anywhere; or, where that costs no CTA more than
-  // kJoinTiles tiles, the same shares cut at the nearest unit (no partials, no
-  // join).
+  // Equal shares over as many CTAs as there are tiles, cut at the nearest unit
+  // (no partials, no join), where that costs no CTA more than kJoinTiles tiles;
+  // otherwise cut anywhere, kMinTiles tiles a CTA at least.
   __shared__ long long s_cut[kMaxScheduleCtas + 1];
-  int over = 0;
-  for (int c = tid; c <= ctas; c += 1024) {
-    long long x = share_lo(tiles, ctas, c);
-    if (c > 0 && c < ctas) {
-      int nt;
-      const int4 st = find(x, nt);
-      x += 2 * st.w >= nt ? nt - st.w : -st.w;
+  int ctas = 0;
+  bool cut = true;
+#pragma unroll 1
+  for (int least = 1; cut && least <= FrameCfg<D>::kMinTiles; least += FrameCfg<D>::kMinTiles - 1) {
+    const long long want = (tiles + least - 1) / least;
+    ctas = static_cast<int>(want < fs.ctas ? want : fs.ctas);
+    for (int c = tid; c <= ctas; c += 1024) {
+      long long x = share_lo(tiles, max(ctas, 1), c);
+      if (c > 0 && c < ctas) {
+        int nt;
+        const int4 st = find(x, nt);
+        x += 2 * st.w >= nt ? nt - st.w : -st.w;
+      }
+      s_cut[c] = x;
     }
-    s_cut[c] = x;
+    __syncthreads();
+    const long long share = ctas > 0 ? (tiles + ctas - 1) / ctas : 0;
+    int over = 0;
+    for (int c = tid; c < ctas; c += 1024) over |= s_cut[c + 1] - s_cut[c] > share + kJoinTiles;
+    cut = __syncthreads_or(over);
   }
-  __syncthreads();
-  const long long share = ctas > 0 ? (tiles + ctas - 1) / ctas : 0;
-  for (int c = tid; c < ctas; c += 1024) over |= s_cut[c + 1] - s_cut[c] > share + kJoinTiles;
-  const bool cut = __syncthreads_or(over);
   for (int c = tid; c < fs.ctas; c += 1024) {
     int4 st = make_int4(0, 0, 0, 0);
     int n = 0;
@@ -345,6 +351,10 @@ __global__ void __launch_bounds__(1024, 1)
     }
     fs.starts[c] = st;
     fs.n[c] = n;
+  }
+  if (tid == 0) {
+    fs.meta[0] = tiles;
+    fs.meta[1] = ctas;
   }
 }
 
@@ -1005,11 +1015,11 @@ __global__ void __launch_bounds__(512, 1)
             make_float2(m, l);
       if (threadIdx.x == 0 && si.starts && !whole) {
         // this unit's parts: this CTA, then every one up to the last tile
-        int parts = 1, rest = si.rest;
-        for (int c = blockIdx.x + 1; rest > 0 && c < static_cast<int>(gridDim.x); ++c) {
-          ++parts;
-          rest -= fs.n[c];
-        }
+        // (a unit is split by equal shares only)
+        const long long tiles = fs.meta[0];
+        const int ctas = static_cast<int>(fs.meta[1]);
+        const long long x_end = share_lo(tiles, ctas, blockIdx.x + 1) + si.rest;
+        const int parts = share_owner(tiles, ctas, x_end - 1) - blockIdx.x + 1;
         int* desc = p.desc + 8 * blockIdx.x;
         desc[1] = si.c0;
         desc[2] = si.unit_row;
@@ -1042,10 +1052,12 @@ __global__ void __launch_bounds__(128)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   using C = FrameCfg<D>;
   constexpr int V = D / 32;  // columns of a lane
-  const int* desc = p.desc + 8 * blockIdx.x;
-  const int parts = desc[0];
+  // (the partials are read past L1: this grid may have started before they were
+  // written)
+  const int4 d0 = __ldcg(reinterpret_cast<const int4*>(p.desc + 8 * blockIdx.x));
+  const int parts = d0.x, c0 = d0.y, unit_row = d0.z, h = d0.w;
   if (parts == 0) return;
-  const int c0 = desc[1], unit_row = desc[2], h = desc[3], rows = desc[4];
+  const int rows = __ldcg(p.desc + 8 * blockIdx.x + 4);
   const int lane = threadIdx.x & 31;
   const int first = blockIdx.y * 4 + (threadIdx.x >> 5);
   auto part_of = [&](int i) {
@@ -1058,7 +1070,7 @@ __global__ void __launch_bounds__(128)
     for (int i0 = 0; i0 < parts; i0 += 32) {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (i0 + lane < parts)
-        ml = *reinterpret_cast<const float2*>(part_of(i0 + lane) + C::kRows * D + 2 * rho);
+        ml = __ldcg(reinterpret_cast<const float2*>(part_of(i0 + lane) + C::kRows * D + 2 * rho));
       float mn = fmaxf(m, ml.x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
@@ -1078,13 +1090,13 @@ __global__ void __launch_bounds__(128)
         const float wi = __shfl_sync(0xffffffffu, w, i);
         const float* x = part_of(i0 + i) + rho * D + lane * V;
         if constexpr (V == 4) {
-          const float4 o = __ldg(reinterpret_cast<const float4*>(x));
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(x));
           acc[0] = fmaf(o.x, wi, acc[0]);
           acc[1] = fmaf(o.y, wi, acc[1]);
           acc[2] = fmaf(o.z, wi, acc[2]);
           acc[3] = fmaf(o.w, wi, acc[3]);
         } else {
-          const float2 o = __ldg(reinterpret_cast<const float2*>(x));
+          const float2 o = __ldcg(reinterpret_cast<const float2*>(x));
           acc[0] = fmaf(o.x, wi, acc[0]);
           acc[1] = fmaf(o.y, wi, acc[1]);
         }

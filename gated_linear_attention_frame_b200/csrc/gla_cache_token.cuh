@@ -123,6 +123,11 @@ __device__ __forceinline__ int64_t share_lo(int64_t total, int ctas, int c) {
   return total / ctas * c + total % ctas * c / ctas;
 }
 
+// The CTA whose share holds block x.
+__device__ __forceinline__ int share_owner(int64_t total, int ctas, int64_t x) {
+  return static_cast<int>(((x + 1) * ctas - 1) / total);
+}
+
 // A query row is multiplied by 2^row_exponent before it becomes fp16: 14 - E for
 // a largest magnitude of bf16 exponent E (0 for zero and non-finite rows).
 __device__ __forceinline__ int row_exponent(uint32_t amax_bits) {
@@ -774,9 +779,7 @@ __global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
       }
     }
     if (tid == 0 && starts && !ends) {
-      int parts = 1;
-      const long long x_end = cur.x_unit + cur.v.nb;
-      for (int c = blockIdx.x + 1; c < ctas && share_lo(total, ctas, c) < x_end; ++c) ++parts;
+      const int parts = share_owner(total, ctas, cur.x_unit + cur.v.nb - 1) - blockIdx.x + 1;
       desc[1] = cur.s.c0 + t0;
       desc[2] = g0;
       desc[3] = cur.h;
@@ -790,74 +793,91 @@ __global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
 // Joins the partials of a unit that several CTAs share: CTA x of the grid takes
 // the unit (if any) that begins in CTA x of the attention kernel and goes on
 // after it; its parts are partial 1 of that CTA and partial 0 of the next
-// ones.  blockIdx.y: a query row.  Four (eight at d = 64) groups of threads
-// take every fourth (eighth) part; the sums are joined in a fixed order.
+// ones.  blockIdx.y: a query row.  Warp w takes parts w, w + 4, ..: 32 (m, l) at
+// a time, one a lane, then their O rows, eight loads in flight; the four warps
+// are joined in a fixed order.
 template <int D, int R>
 __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kGroups = 128 / (D / 4);
-  constexpr int part_floats = TokenCfg<D, R>::kPartFloats, part_rows = R;
-  __shared__ float4 s_acc[128];
-  __shared__ float s_m[kGroups], s_l[kGroups];
-  const int* desc = p.desc + 8 * blockIdx.x;
-  const int parts = desc[0], rho = blockIdx.y;
-  if (parts == 0 || rho >= desc[4]) return;
-  const int grp = threadIdx.x / (D / 4), c4 = threadIdx.x % (D / 4);
+  constexpr int kFloats = TokenCfg<D, R>::kPartFloats;
+  constexpr int V = D / 32;  // columns of a lane
+  __shared__ float s_acc[4][D];
+  __shared__ float2 s_ml[4];
+  // (the partials are read past L1: this grid may have started before they were
+  // written)
+  const int4 d0 = __ldcg(reinterpret_cast<const int4*>(p.desc + 8 * blockIdx.x));
+  const int rows = __ldcg(p.desc + 8 * blockIdx.x + 4);
+  const int parts = d0.x, rho = blockIdx.y;
+  if (parts == 0 || rho >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto part_of = [&](int i) {
-    return p.part + (i == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + i)) * part_floats;
+    return p.part + (i == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + i)) * kFloats;
   };
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = grp; i < parts; i += kGroups) {
-    const float* a = part_of(i);
-    const float2 ml = *reinterpret_cast<const float2*>(a + part_rows * D + 2 * rho);
-    if (ml.x == -INFINITY) continue;  // uniform over the group
-    const float4 x = *reinterpret_cast<const float4*>(a + rho * D + c4 * 4);
-    const float mn = fmaxf(m, ml.x);
-    const float f0 = m == -INFINITY ? 0.f : exp2f(m - mn), f1 = exp2f(ml.x - mn);
+  float m = -INFINITY, l = 0.f, acc[V] = {};
+  for (int i0 = warp; i0 < parts; i0 += 128) {
+    const int mine = i0 + 4 * lane;  // this lane's part
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (mine < parts) ml = __ldcg(reinterpret_cast<const float2*>(part_of(mine) + R * D + 2 * rho));
+    float mn = fmaxf(m, ml.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    if (mn == -INFINITY) continue;  // uniform
+    const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
+    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+    float ls = ml.y * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
     m = mn;
-    l = l * f0 + ml.y * f1;
-    acc.x = acc.x * f0 + x.x * f1;
-    acc.y = acc.y * f0 + x.y * f1;
-    acc.z = acc.z * f0 + x.z * f1;
-    acc.w = acc.w * f0 + x.w * f1;
+    l = l * f + ls;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= f;
+    const int n = min(32, (parts - i0 + 3) / 4);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* x = part_of(i0 + 4 * i) + rho * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(x));
+        acc[0] = fmaf(o.x, wi, acc[0]);
+        acc[1] = fmaf(o.y, wi, acc[1]);
+        acc[2] = fmaf(o.z, wi, acc[2]);
+        acc[3] = fmaf(o.w, wi, acc[3]);
+      } else {
+        const float2 o = __ldcg(reinterpret_cast<const float2*>(x));
+        acc[0] = fmaf(o.x, wi, acc[0]);
+        acc[1] = fmaf(o.y, wi, acc[1]);
+      }
+    }
   }
-  s_acc[threadIdx.x] = acc;
-  if (c4 == 0) {
-    s_m[grp] = m;
-    s_l[grp] = l;
-  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_acc[warp][lane * V + v] = acc[v];
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
   __syncthreads();
-  if (grp != 0) return;
+  const int col = threadIdx.x * 2;
+  if (col >= D) return;
   float mm = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) mm = fmaxf(mm, s_m[i]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  l = 0.f;
+  for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_ml[w].x);
+  float x0 = 0.f, x1 = 0.f, ls = 0.f;
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const float f = s_m[i] == -INFINITY ? 0.f : exp2f(s_m[i] - mm);
-    const float4 x = s_acc[i * (D / 4) + c4];
-    l += s_l[i] * f;
-    o.x += x.x * f;
-    o.y += x.y * f;
-    o.z += x.z * f;
-    o.w += x.w * f;
+  for (int w = 0; w < 4; ++w) {
+    const float f = s_ml[w].x == -INFINITY ? 0.f : exp2f(s_ml[w].x - mm);
+    ls += s_ml[w].y * f;
+    x0 += s_acc[w][col] * f;
+    x1 += s_acc[w][col + 1] * f;
   }
-  const float rl = mm == -INFINITY ? 0.f : 1.0f / l;
-  const int g = desc[2] + rho, rt = g / p.G;  // g0 = 0 unless a token has several tiles
+  const float rl = mm == -INFINITY ? 0.f : 1.0f / ls;
+  x0 *= rl;
+  x1 *= rl;
+  const int g = d0.z + rho, rt = g / p.G;  // d0.z = 0 unless a token has several tiles
   const int64_t off =
-      ((static_cast<int64_t>(desc[1]) + rt) * p.H + desc[3] * p.G + (g - rt * p.G)) * D + c4 * 4;
-  float x[4] = {o.x * rl, o.y * rl, o.z * rl, o.w * rl};
+      ((static_cast<int64_t>(d0.y) + rt) * p.H + d0.w * p.G + (g - rt * p.G)) * D + col;
   if (p.z != nullptr) {
-    const uint2 zw = *reinterpret_cast<const uint2*>(p.z + off);
-    const float zf[4] = {bf16lo_to_f32(zw.x), bf16hi_to_f32(zw.x), bf16lo_to_f32(zw.y),
-                         bf16hi_to_f32(zw.y)};
-#pragma unroll
-    for (int y = 0; y < 4; ++y) x[y] *= 1.0f / (1.0f + expf(-zf[y]));
+    const uint32_t z = *reinterpret_cast<const uint32_t*>(p.z + off);
+    x0 *= 1.0f / (1.0f + __expf(-bf16lo_to_f32(z)));
+    x1 *= 1.0f / (1.0f + __expf(-bf16hi_to_f32(z)));
   }
-  *reinterpret_cast<uint2*>(p.out + off) =
-      make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+  *reinterpret_cast<uint32_t*>(p.out + off) = pack_bf16x2(x0, x1);
 }
 
 }  // namespace gla
