@@ -1128,6 +1128,7 @@ int run_cache_token(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
   using C = gla::TokenCfg<D, R>;
   p.tile_t = p.G <= R ? R / p.G : 1;
   p.tile_c = p.G <= R ? 1 : (p.G + R - 1) / R;
+  p.by_tile = gla::FastDiv::make(static_cast<uint32_t>(p.tile_c > 1 ? p.tile_c : p.tile_t));
   const int grid = di.sms * C::kCtasPerSm;
   const int64_t desc_bytes = align256(static_cast<int64_t>(grid) * 32);
   const int64_t part_bytes = static_cast<int64_t>(grid) * 2 * C::kPartFloats * 4;
@@ -1232,6 +1233,7 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
     if (!aligned(x, 4)) return GLA_ERR_ALIGN;
   p.G = p.H / p.Hkv;
   p.p_shift = page_shift(P);
+  p.by_f = gla::FastDiv::make(static_cast<uint32_t>(p.F));
   p.sl2 = static_cast<float>(1.4426950408889634 * scale);
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;

@@ -38,6 +38,28 @@
 
 namespace gla {
 
+// Division of 0 <= n < 2^31 by d >= 1 as a multiplication and a shift (m = 2^32
+// (2^s - d) / d + 1, s = ceil(log2 d); exact for every 32-bit n): the kernels
+// divide by the frame and the tile in many places, and a division is 25
+// instructions.
+struct FastDiv {
+  uint32_t m, s;
+  __host__ static FastDiv make(uint32_t d) {
+    FastDiv f{0, 0};
+    while ((uint64_t(1) << f.s) < d) ++f.s;
+    f.m = static_cast<uint32_t>((((uint64_t(1) << f.s) - d) << 32) / d + 1);
+    return f;
+  }
+  __host__ __device__ __forceinline__ int div(int n) const {
+#ifdef __CUDA_ARCH__
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), m) + static_cast<uint32_t>(n)) >> s);
+#else
+    return static_cast<int>(((static_cast<uint64_t>(static_cast<uint32_t>(n)) * m >> 32) +
+                             static_cast<uint32_t>(n)) >> s);
+#endif
+  }
+};
+
 struct CacheAttnParams {
   const __nv_bfloat16* q;
   const uint8_t *k8, *v8;
@@ -52,6 +74,7 @@ struct CacheAttnParams {
   // token kernel: a tile of 16 rows holds `tile_t` tokens (all G heads of each),
   // or, where G > 16, one of `tile_c` parts of one token's heads
   int tile_t, tile_c;
+  FastDiv by_f, by_tile;  // by F; by tile_t, or tile_c where that is not 1
   // split units: per CTA two partials of kPartRows rows (fp32 O, then m, l)
   // and one descriptor
   float* part;
@@ -96,13 +119,14 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheAttnParams& p, int r) {
 // Upper and lower end of the keys of a query at position pos (negative: none).
 __device__ __forceinline__ int key_hi(const CacheAttnParams& p, const CacheSeq& s, int pos) {
   if (pos < 0) return 0;
-  const int64_t e = (static_cast<int64_t>(pos / p.F) + 1) * p.F;
-  return e < s.len ? static_cast<int>(e) : s.len;
+  const int rest = pos - p.by_f.div(pos) * p.F;  // within the frame
+  const uint32_t e = static_cast<uint32_t>(pos) + static_cast<uint32_t>(p.F - rest);  // < 2^32
+  return static_cast<int>(min(e, static_cast<uint32_t>(s.len)));
 }
 __device__ __forceinline__ int key_lo(const CacheAttnParams& p, int pos) {
   if (p.W == 0 || pos < 0) return 0;
-  const int64_t e = (static_cast<int64_t>(pos / p.F) - p.W + 1) * p.F;
-  return e > 0 ? static_cast<int>(e) : 0;
+  const int q = p.by_f.div(pos);
+  return q < p.W ? 0 : (q - p.W + 1) * p.F;  // at most pos
 }
 
 template <int BK>
@@ -119,8 +143,10 @@ __device__ __forceinline__ CacheSpan cache_span(const CacheAttnParams& p, const 
 }
 
 // Contiguous share of CTA c of `total` blocks dealt out over `ctas` CTAs.
+// (total * ctas < 2^63: blocks are counted in pages of 32-bit slots.)
 __device__ __forceinline__ int64_t share_lo(int64_t total, int ctas, int c) {
-  return total / ctas * c + total % ctas * c / ctas;
+  return static_cast<int64_t>(static_cast<uint64_t>(total) * static_cast<uint32_t>(c) /
+                              static_cast<uint32_t>(ctas));
 }
 
 // The CTA whose share holds block x.
@@ -249,10 +275,10 @@ __global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
   // query tiles of a sequence, and the keys one of them sees
   const int gm = (65536 + p.G - 1) / p.G;  // see small_div
   auto tiles_of = [&](const CacheSeq& s) {
-    return p.tile_c > 1 ? s.n * p.tile_c : (s.n + p.tile_t - 1) / p.tile_t;
+    return p.tile_c > 1 ? s.n * p.tile_c : p.by_tile.div(s.n + p.tile_t - 1);
   };
   auto first_token = [&](int tile) {
-    return p.tile_c > 1 ? tile / p.tile_c : tile * p.tile_t;
+    return p.tile_c > 1 ? p.by_tile.div(tile) : tile * p.tile_t;
   };
   auto span_of = [&](const CacheSeq& s, int tile) {
     const int t = first_token(tile);
@@ -288,8 +314,12 @@ __global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
   const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
   if (tid == 0) desc[0] = 0;  // nothing to join unless a unit goes on past this CTA
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long x0 = share_lo(total, ctas, blockIdx.x);
-  const long long x1 = share_lo(total, ctas, blockIdx.x + 1);
+  long long x0 = 0, x1 = 0;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {  // one copy of the division
+    x0 = x1;
+    x1 = share_lo(total, ctas, blockIdx.x + c);
+  }
 
   // A unit, and this warp's place in the part [k, k_end) of its blocks that
   // belongs to this CTA.
