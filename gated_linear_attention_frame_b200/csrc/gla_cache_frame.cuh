@@ -18,8 +18,8 @@
 // turn them into fp16 and write them in the swizzled operand layout.  All 128
 // keys of a tile take one key scale and one value scale, the largest of its
 // pages': the converters multiply the codes of the other pages by the ratio, a
-// power of two (exact while it is at least 2^-15; beyond, below 2^-33 of the
-// largest value).  Keys that no row of the unit sees become zeros there, so
+// power of two (exact while it is at least 2^-15; a page 2^25 or more below
+// another of its tile counts as zeros).  Keys that no row of the unit sees become zeros there, so
 // stray pages and NaN codes never reach a product.
 //   S_h = Q_h K^T   A = Q half [128 x d] K-major, B = K tile [128 keys] K-major
 //   O_h += P_h V    A = P_h in TMEM (fp16, over the columns of S_h),
@@ -181,7 +181,8 @@ struct SegInfo {
   int len;           // keys of the sequence
   int lo, hi, sink;  // visible keys, as in CacheSpan
   int whole, starts; // the segment is the unit; it holds the unit's first tile
-  int c0, unit_row, h, rest;  // for the join: first packed row, first row, head, tiles after
+  int c0, t_unit, h, rest;  // for the join: packed row and token of the unit's start, head, tiles
+                            // after the segment
 };
 static_assert(sizeof(SegInfo) == 56, "one slot of the segment ring");
 
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(512, 1)
             si.whole = cur.t0 == 0 && cur.t1 == cur.v.nb;
             si.starts = cur.t0 == 0;
             si.c0 = cur.s.c0;
-            si.unit_row = t_unit * p.G;
+            si.t_unit = t_unit;
             si.h = cur.h;
             si.rest = cur.v.nb - cur.t1;
           }
@@ -1022,7 +1023,7 @@ __global__ void __launch_bounds__(512, 1)
         const int parts = share_owner(tiles, ctas, x_end - 1) - blockIdx.x + 1;
         int* desc = p.desc + 8 * blockIdx.x;
         desc[1] = si.c0;
-        desc[2] = si.unit_row;
+        desc[2] = si.t_unit;
         desc[3] = si.h;
         desc[4] = min(2 * fs.TQ, si.tokens) * p.G;
         desc[0] = parts;
@@ -1055,7 +1056,7 @@ __global__ void __launch_bounds__(128)
   // (the partials are read past L1: this grid may have started before they were
   // written)
   const int4 d0 = __ldcg(reinterpret_cast<const int4*>(p.desc + 8 * blockIdx.x));
-  const int parts = d0.x, c0 = d0.y, unit_row = d0.z, h = d0.w;
+  const int parts = d0.x, c0 = d0.y, t_unit = d0.z, h = d0.w;
   if (parts == 0) return;
   const int rows = __ldcg(p.desc + 8 * blockIdx.x + 4);
   const int lane = threadIdx.x & 31;
@@ -1074,9 +1075,10 @@ __global__ void __launch_bounds__(128)
       float mn = fmaxf(m, ml.x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      if (mn == -INFINITY) continue;  // uniform
+      // nothing visible in these parts, unless the row is NaN (l is, and w below)
+      if (mn == -INFINITY && !__any_sync(0xffffffffu, ml.y != ml.y)) continue;
       const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+      const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - mn);
       float ls = ml.y * w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
@@ -1103,9 +1105,8 @@ __global__ void __launch_bounds__(128)
       }
     }
     const float rl = m == -INFINITY ? 0.f : 1.0f / l;
-    const int row = unit_row + r;
     const int64_t off =
-        ((static_cast<int64_t>(c0) + row / p.G) * p.H + h * p.G + row % p.G) * D + lane * V;
+        ((static_cast<int64_t>(c0) + t_unit + r / p.G) * p.H + h * p.G + r % p.G) * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       float x0 = acc[v] * rl, x1 = acc[v + 1] * rl;

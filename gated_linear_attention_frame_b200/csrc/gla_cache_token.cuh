@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(128, (TokenCfg<D, R>::kCtasPerSm))
       ll[e] = 0.f;
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w)
-        ll[e] += a[w].x == -INFINITY ? 0.f : a[w].y * ex2_approx(a[w].x - mm[e]);
+        // (m = -inf: l is 0, or NaN for a row that is not finite: it goes on)
+        ll[e] += a[w].x == -INFINITY ? a[w].y : a[w].y * ex2_approx(a[w].x - mm[e]);
       const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - mm[e]);
 #pragma unroll
       for (int n = 0; n < NO; ++n)
@@ -851,9 +852,10 @@ __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnP
     float mn = fmaxf(m, ml.x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    if (mn == -INFINITY) continue;  // uniform
+    // nothing visible in these parts, unless the row is NaN (l is, and w below)
+    if (mn == -INFINITY && !__any_sync(0xffffffffu, ml.y != ml.y)) continue;
     const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-    const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+    const float w = ml.x == -INFINITY ? ml.y : exp2f(ml.x - mn);
     float ls = ml.y * w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
@@ -891,7 +893,7 @@ __global__ void __launch_bounds__(128) gla_cache_combine_kernel(const CacheAttnP
   float x0 = 0.f, x1 = 0.f, ls = 0.f;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float f = s_ml[w].x == -INFINITY ? 0.f : exp2f(s_ml[w].x - mm);
+    const float f = s_ml[w].x == -INFINITY ? s_ml[w].y : exp2f(s_ml[w].x - mm);
     ls += s_ml[w].y * f;
     x0 += s_acc[w][col] * f;
     x1 += s_acc[w][col + 1] * f;

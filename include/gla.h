@@ -273,8 +273,8 @@ int gla_softmax_anchor_step(const void* q, const void* k, const void* v, const v
  * (bits add up).  With a nonzero status nothing changes: lens_out, held_out and
  * free_count_out equal their inputs, cu_tokens is 0 and slots are -1, so that
  * a store and an attention behind it do nothing.
- * lens_out, held_out and free_count_out may be the inputs' pointers.  The call
- * is one kernel, takes no workspace and may be captured into a CUDA graph.
+ * lens_out, held_out and free_count_out may be the inputs' pointers.  One
+ * kernel, two above 8192 rows; no workspace; may be captured into a CUDA graph.
  */
 int gla_cache_plan(const int* lens, const int* held, const int* new_lens, const int* free_count,
                    int* free_pages, int* block_table, int* lens_out, int* held_out,
@@ -327,7 +327,10 @@ int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu
  * Precision: e4m3 codes enter the products exactly, q scaled by a power of two
  * per row (exact), the softmax weights rounded to fp16; scores, sums and
  * outputs accumulate in fp32, out is rounded once to bf16.  The same inputs
- * give the same bits.
+ * give the same bits.  In calls of more than 64 query rows a sequence and
+ * key/value head, 128 neighbouring keys share one scale inside the kernel: a
+ * page whose scale is within 2^15 of the largest among them enters exactly, one
+ * 2^25 or more below it counts as zeros.
  * Memory: a workspace from the library's pool, freed on `stream`.
  */
 int gla_cache_attention(const void* q, const void* k_cache, const void* v_cache,
@@ -593,7 +596,7 @@ const char* gla_error_string(int status);
  * output is then invalid.  Bit 0: state-increment kernel, bit 1: output
  * kernel, bit 2: forward scan, bit 3: reverse scan, bit 4: key/value
  * gradient kernel, bit 5: query gradient kernel, bit 6: delta-rule scan,
- * bit 7: softmax anchor kernel.
+ * bit 7: softmax anchor kernel, bit 8: cached attention of many queries.
  * `code` is a host pointer.
  * Returns GLA_OK or GLA_ERR_LAUNCH.
  */

@@ -477,3 +477,105 @@ def test_wrappers_refuse_on_the_gpu(gla):
         gla.cache_plan(c, torch.ones(2, dtype=torch.int64, device="cuda"), 2)
     with pytest.raises(ValueError, match="out must"):
         gla.cache_attention(c, plan, x, out=x[:1])
+
+
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+def test_a_broken_query_row_stays_alone(gla, max_new):
+    """NaN or infinity in one query row: that row alone is not finite."""
+    P, d, H = 32, 128, 2
+    c = Cache(8, 1, P, d, 8, range(8))
+    c.add(0)
+    c.step(gla, [200], bf((200, 1, d), 1), bf((200, 1, d), 2))
+    q = bf((40, H, d), 3).cuda()
+    args = (c.k8, c.v8, c.ks, c.vs, c.tables(), ints(c.lens), ints([0, 40]), None)
+    tail = (1, 40, max_new, H, 1, d, 8, P, 8, 1, 0, 0, d ** -0.5)
+    good, out = torch.empty_like(q), torch.empty_like(q)
+    gla.gla_cache_attention(q, *args, good, *tail)
+    q[7, 1, 5], q[20, 0, 9] = float("nan"), float("inf")
+    gla.gla_cache_attention(q, *args, out, *tail)
+    rows = torch.ones(40, H, dtype=torch.bool, device="cuda")
+    rows[7, 1] = rows[20, 0] = False
+    assert torch.isfinite(good).all() and torch.isfinite(out[rows]).all()
+    # a rescale that the broken row sets off may move the others by a rounding
+    assert torch.allclose(out[rows].float(), good[rows].float(), rtol=2 ** -6, atol=2 ** -8)
+    assert not torch.isfinite(out[7, 1]).any()
+
+
+def test_neighbouring_pages_of_different_scale(gla):
+    """Keys and values of pages whose scales differ by up to 2^12 within 128
+    keys: the tile's common scale is exact."""
+    P, d = 16, 128
+    c = Cache(16, 1, P, d, 16, range(16))
+    c.add(0)
+    step = torch.exp2(-((torch.arange(230) // P * 5) % 13).float())[:, None, None]
+    c.step(gla, [230], (bf((230, 1, d), 1).float() * step).bfloat16(),
+           (bf((230, 1, d), 2).float() * step.flip(0)).bfloat16())
+    for m in (1, 9, 1 << 20):
+        check_attention(gla, c, [100], 1, 1, 0, 0, False, 3, max_new=m, qscale=4.0)
+
+
+def test_frames_in_two_graphs_at_once(gla):
+    """Whole frame steps (plan, store, attention with split units) captured
+    twice; the replays run together on two streams and give the eager bits."""
+    P, d, Hkv, H, T, pages = 64, 128, 2, 4, 4100, 300
+    data = [bf((2 * T, h, d), 5 + e).cuda() for e, h in enumerate((Hkv, Hkv, H))]
+    mk = lambda: gla.rollout_cache(2, pages, Hkv, d, 200, page_tokens=P, frame_tokens=T,  # noqa: E731
+                                   window_frames=2, n_sink=100)
+
+    def step(c, new, k, v, q, out):
+        plan = gla.cache_plan(c, new, 2 * T)  # above 8192 rows: two launches
+        gla.cache_store(c, plan, k, v)
+        gla.cache_attention(c, plan, q, out=out, max_new=T)
+        return plan
+
+    new = ints([T, T])
+    c = mk()
+    want = []
+    for _ in range(2):
+        want.append(torch.empty_like(data[2]))
+        step(c, new, *data, want[-1])
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(2):
+        c, out = mk(), torch.empty_like(data[2])
+        keep = [t.clone() for t in (c.lens, c.held, c.block_table, c.free_pages, c.free_count)]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step(c, new, *data, out)
+        side.synchronize()
+        for t, x in zip((c.lens, c.held, c.block_table, c.free_pages, c.free_count), keep):
+            t.copy_(x)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            plan = step(c, new, *data, out)
+        for t, x in zip((c.lens, c.held, c.block_table, c.free_pages, c.free_count), keep):
+            t.copy_(x)
+        runs.append((g, out, plan, torch.cuda.Stream(), c))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g, _, _, s, _ in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, out, plan, _, _ in runs:
+            assert plan.status.item() == 0
+            assert torch.equal(out, want[i])
+
+
+def test_many_tiny_sequences_and_wide_groups(gla):
+    """More sequences than CTAs, most of them idle; 128 and 20 heads a group."""
+    rng = random.Random(5)
+    P, d = 16, 64
+    lens = [rng.choice([0, 1, 5, 17]) for _ in range(700)]
+    new = [min(n, rng.choice([0, 0, 1])) for n in lens]
+    pages = sum(-(-n // P) for n in lens) + 1
+    c = Cache(pages, 1, P, d, 2, range(pages))
+    for _ in lens:
+        c.add(0)
+    n = sum(lens)
+    c.step(gla, lens, bf((n, 1, d), 1), bf((n, 1, d), 2))
+    for G in (1, 20, 128):
+        for m in (1, 1 << 20):
+            check_attention(gla, c, new, G, 1, 0, 0, False, G, max_new=m)
