@@ -1089,7 +1089,8 @@ int cache_store_impl(const gla::StoreParams& p, int d, int P, cudaStream_t strea
     if (!aligned(x, 4)) return GLA_ERR_ALIGN;
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;
-  // at most one item for each page the tokens can touch, head and tensor
+  // at most one item for each page the tokens can touch, head and tensor (or
+  // pair of tensors: the surplus CTAs find nothing)
   const int64_t runs = static_cast<int64_t>(p.tokens) / P + 2 * static_cast<int64_t>(p.R);
   const int64_t items = (runs < p.tokens ? runs : p.tokens) * p.H * 2;
   const StoreChoice k = d == 64 ? store_kernel<64>(P) : store_kernel<128>(P);

@@ -354,7 +354,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 }
 
 // One work item = the new tokens that one sequence adds to one page, for one
-// head and one of K and V: at most P rows of d values, read once into
+// head and one of K and V (small pages: both): at most P rows of d values, read once into
 // registers (the maximum needs all of them before the first code), coded and
 // written once.  Items are dealt out with the heads fastest, so that CTAs of
 // neighbouring items read whole token rows together.  128 threads keep P d / 8
@@ -366,6 +366,9 @@ struct StoreCfg {
   static constexpr int kRowChunks = D / 8;  // 16-byte chunks of a token row
   static constexpr int kRowsPerPass = kStoreThreads / kRowChunks;
   static constexpr int kPasses = P / kRowsPerPass;
+  // tensors of an item: with few loads in one, both, so that enough are in flight
+  // (frames of 1560 tokens, pages of 16: 18.4 -> 16.4 us)
+  static constexpr int kTensors = kPasses <= 4 ? 2 : 1;
   // CTAs of an SM: their loads together cover HBM's latency
   static constexpr int kPerSm = kPasses >= 16 ? 4 : (kPasses >= 8 ? 6 : (kPasses >= 4 ? 8 : 12));
 };
@@ -379,7 +382,8 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
   int* s_c0 = s_items + p.R + 1;    // [R + 1] first packed row of each sequence
   int* s_old = s_c0 + p.R + 1;      // [R] tokens it held before
   __shared__ long long scratch[33];
-  __shared__ uint32_t s_max[2][kStoreThreads / 32];
+  constexpr int kTensors = C::kTensors;
+  __shared__ uint32_t s_max[2][kTensors][kStoreThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int col = tid % C::kRowChunks, row0 = tid / C::kRowChunks;
   {
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
     int t0, m, h, slot;
     bool is_v;
   };
-  const unsigned heads2 = 2u * p.H;
+  const unsigned heads2 = (kTensors == 2 ? 1u : 2u) * p.H;  // items of a page
   auto locate = [&](int64_t it) {
     Item x;
     const int run = static_cast<int>(static_cast<uint64_t>(it) / heads2);
@@ -436,91 +440,110 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
   if (blockIdx.x < items) next = locate(blockIdx.x);
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x, flip ^= 1) {
     const Item cur = next;
-    const bool is_v = cur.is_v;
     const int h = cur.h;
     const int page = cur.slot >= 0 ? cur.slot / P : p.pages;
     const int at = cur.slot >= 0 ? cur.slot % P : 0;
     // a slot outside the cache: nothing to write
     const int m = page < p.pages ? min(cur.m, P - at) : 0;
+    auto is_v = [&](int w) { return kTensors == 2 ? w == 1 : cur.is_v; };
 
-    const __nv_bfloat16* src =
-        (is_v ? p.v : p.k) + (static_cast<int64_t>(cur.t0) * p.H + h) * D + col * 8;
-    uint4 x[kPasses];
+    const int64_t from = (static_cast<int64_t>(cur.t0) * p.H + h) * D + col * 8;
+    uint4 x[kTensors][kPasses];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int row = row0 + i * kRowsPerPass;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (row < m)
-        x[i] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(row) * p.H * D));
+    for (int w = 0; w < kTensors; ++w) {
+      const __nv_bfloat16* src = (is_v(w) ? p.v : p.k) + from;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = row0 + i * kRowsPerPass;
+        x[w][i] = make_uint4(0, 0, 0, 0);
+        if (row < m)
+          x[w][i] =
+              __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(row) * p.H * D));
+      }
     }
     if (it + gridDim.x < items) next = locate(it + gridDim.x);
     const int64_t blk = static_cast<int64_t>(m > 0 ? page : 0) * p.H + h;
-    float* scale_p = (is_v ? p.vs : p.ks) + blk;
-    const float was = at > 0 && m > 0 ? *scale_p : 0.f;
-    // largest magnitude (packed 16-bit maxima of the bf16 bits)
-    uint32_t mx = 0;
+    float was[kTensors];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                                 __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
-    }
-    mx = max(mx & 0xFFFFu, mx >> 16);
-    if (mx >= 0x7F80u) {
-      // some are not finite: they do not count for the scale; NaN becomes 0,
-      // infinities stay for the saturating conversion
-      mx = 0;
+    for (int w = 0; w < kTensors; ++w)
+      was[w] = at > 0 && m > 0 ? (is_v(w) ? p.vs : p.ks)[blk] : 0.f;
+#pragma unroll
+    for (int w = 0; w < kTensors; ++w) {
+      // largest magnitude (packed 16-bit maxima of the bf16 bits)
+      uint32_t mx = 0;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+        const uint4& y = x[w][i];
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu),
+                                   __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu)));
+      }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      if (mx >= 0x7F80u) {
+        // some are not finite: they do not count for the scale; NaN becomes 0,
+        // infinities stay for the saturating conversion
+        mx = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t lo = w[e] & 0x7FFFu, hi = (w[e] >> 16) & 0x7FFFu;
-          bad += (lo >= 0x7F80u) + (hi >= 0x7F80u);
-          if (lo > 0x7F80u) w[e] &= 0xFFFF0000u;
-          if (hi > 0x7F80u) w[e] &= 0x0000FFFFu;
-          mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        for (int i = 0; i < kPasses; ++i) {
+          uint32_t* y = reinterpret_cast<uint32_t*>(&x[w][i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = y[e] & 0x7FFFu, hi = (y[e] >> 16) & 0x7FFFu;
+            bad += (lo >= 0x7F80u) + (hi >= 0x7F80u);
+            if (lo > 0x7F80u) y[e] &= 0xFFFF0000u;
+            if (hi > 0x7F80u) y[e] &= 0x0000FFFFu;
+            mx = max(mx, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+          }
         }
       }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0) s_max[flip][w][warp] = mx;
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) s_max[flip][warp] = mx;
     __syncthreads();  // the other half of s_max is free again after this barrier
-    mx = max(max(s_max[flip][0], s_max[flip][1]), max(s_max[flip][2], s_max[flip][3]));
     if (m <= 0) continue;  // uniform over the block
-    uint8_t* dst = (is_v ? p.v8 : p.k8) + blk * (P * D);
-    float scale = exp2_int(scale_exponent(mx));
-    if (at > 0) scale = fmaxf(scale, was);
-    // both powers of two: the products below are exact in bf16
-    const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
+    float scale[kTensors];
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int row = row0 + i * kRowsPerPass;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t c[4];
+    for (int w = 0; w < kTensors; ++w) {
+      const uint32_t* sm = s_max[flip][w];
+      const uint32_t mx = max(max(sm[0], sm[1]), max(sm[2], sm[3]));
+      scale[w] = exp2_int(scale_exponent(mx));
+      if (at > 0) scale[w] = fmaxf(scale[w], was[w]);
+      uint8_t* dst = (is_v(w) ? p.v8 : p.k8) + blk * (P * D);
+      // both powers of two: the products below are exact in bf16
+      const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale[w]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[e]), inv);
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
-        c[e] = pack_e4m3x2(bf16lo_to_f32(v), bf16hi_to_f32(v));
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = row0 + i * kRowsPerPass;
+        const uint32_t y[4] = {x[w][i].x, x[w][i].y, x[w][i].z, x[w][i].w};
+        uint32_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]), inv);
+          const uint32_t v = *reinterpret_cast<const uint32_t*>(&z);
+          c[e] = pack_e4m3x2(bf16lo_to_f32(v), bf16hi_to_f32(v));
+        }
+        if (row < m)
+          *reinterpret_cast<uint2*>(dst + (at + row) * D + col * 8) =
+              make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
       }
-      if (row < m)
-        *reinterpret_cast<uint2*>(dst + (at + row) * D + col * 8) =
-            make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    }
-    if (at > 0 && scale != was) {  // the page's scale grew: its earlier tokens are coded again
-      const float ratio = was / scale;
-      for (int i = tid; i < at * (D / 4); i += kStoreThreads) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(dst) + i;
-        const uint32_t q = *w;
-        const uint32_t f0 = e4m3x2_to_f16x2(q & 0xFFFFu), f1 = e4m3x2_to_f16x2(q >> 16);
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f0));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&f1));
-        *w = pack_e4m3x2(a.x * ratio, a.y * ratio) | (pack_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+      if (at > 0 && scale[w] != was[w]) {  // the scale grew: earlier tokens are coded again
+        const float ratio = was[w] / scale[w];
+        for (int i = tid; i < at * (D / 4); i += kStoreThreads) {
+          uint32_t* y = reinterpret_cast<uint32_t*>(dst) + i;
+          const uint32_t q = *y;
+          const uint32_t f0 = e4m3x2_to_f16x2(q & 0xFFFFu), f1 = e4m3x2_to_f16x2(q >> 16);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&f0));
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&f1));
+          *y = pack_e4m3x2(a.x * ratio, a.y * ratio) |
+               (pack_e4m3x2(b.x * ratio, b.y * ratio) << 16);
+        }
       }
     }
     // every thread has read the old scale before one replaces it
     if (at > 0) __syncthreads();
-    if (tid == 0) *scale_p = scale;
+    if (tid == 0) {
+#pragma unroll
+      for (int w = 0; w < kTensors; ++w) (is_v(w) ? p.vs : p.ks)[blk] = scale[w];
+    }
   }
   if (p.nonfinite != nullptr) {
     bad = __reduce_add_sync(0xffffffffu, bad);
