@@ -217,8 +217,9 @@ def cache_store(cache: RolloutCache, plan: CachePlan, k, v, nonfinite=None, stre
 def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=None, out=None,
                     max_new=None, stream=None):
     """Attention of the step's queries q [tokens, H, d] over the cache (which
-    already holds the step's keys and values); returns out.  `max_new`: the
-    most new tokens of one sequence, if the host knows it (default: tokens)."""
+    already holds the step's keys and values); returns out.  `max_new`: about
+    the most new tokens of one sequence, as far as the host knows; it picks the
+    kernel, never what is computed (default: the mean, tokens / sequences)."""
     pages, Hkv, P, d = cache.k.shape
     R, max_pages = cache.block_table.shape
     N, H = q.shape[0], q.shape[1]
@@ -232,7 +233,7 @@ def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=
         raise ValueError("out must have q's shape, got %s" % (tuple(out.shape),))
     gla_cache_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.block_table,
                         cache.lens, plan.cu_tokens, gate_z, out, R, N,
-                        N if max_new is None else max_new, H, Hkv, d, pages, P, max_pages,
+                        -(-N // max(R, 1)) if max_new is None else max_new, H, Hkv, d, pages, P, max_pages,
                         cache.frame_tokens, cache.window_frames, cache.n_sink,
                         1.0 / math.sqrt(d) if scale is None else scale, stream)
     return out

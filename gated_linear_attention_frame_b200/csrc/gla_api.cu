@@ -25,6 +25,16 @@
 // gla_softmax_anchor (d = 128) runs gla_softmax_anchor_kernel: one online pass
 // over the key tiles of sinks + window, S = Q K^T and O += P V on tcgen05
 // with the running maxima and sums in the softmax warps.
+// The paged 8-bit rollout cache: gla_cache_plan runs gla_cache_plan_kernel (and
+// gla_cache_slots_kernel above 8192 rows), gla_cache_store
+// gla_cache_store_kernel, and gla_cache_attention, by the query rows of a
+// sequence and key/value head (max_new * H / Hkv), up to 64:
+//   gla_cache_token_kernel     the keys dealt out over all CTAs (mma.sync)
+//   gla_cache_combine_kernel   joins what several CTAs share
+// and above:
+//   gla_cache_schedule_kernel  where each CTA begins
+//   gla_cache_frame_kernel     256 query rows a unit (tcgen05)
+//   gla_cache_join_kernel      joins split units
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
