@@ -231,9 +231,10 @@ def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=
         out = torch.empty_like(q)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape, got %s" % (tuple(out.shape),))
+    if max_new is None:
+        max_new = -(-N // max(R, 1))
     gla_cache_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, cache.block_table,
-                        cache.lens, plan.cu_tokens, gate_z, out, R, N,
-                        -(-N // max(R, 1)) if max_new is None else max_new, H, Hkv, d, pages, P, max_pages,
-                        cache.frame_tokens, cache.window_frames, cache.n_sink,
+                        cache.lens, plan.cu_tokens, gate_z, out, R, N, max_new, H, Hkv, d, pages,
+                        P, max_pages, cache.frame_tokens, cache.window_frames, cache.n_sink,
                         1.0 / math.sqrt(d) if scale is None else scale, stream)
     return out

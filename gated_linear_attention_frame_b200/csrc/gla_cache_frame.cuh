@@ -9,7 +9,7 @@
 // tiles of all units are laid end to end and dealt out evenly to one CTA per
 // SM (gla_cache_schedule_kernel finds where each CTA begins); a unit that ends
 // up in several CTAs leaves a partial (O, m, l) in each, joined by
-// gla_cache_combine_kernel.
+// gla_cache_join_kernel.
 //
 // Both halves of a unit share each key/value tile, because every tile has to
 // be converted first: tcgen05 wants both operands of a product in one type,
@@ -858,7 +858,9 @@ __global__ void __launch_bounds__(512, 1)
           tmem_wait_st();
           tmem_ld_32cols(ts, s[0]);
         }
-        const float fg = rs * info.x;
+        // never 0, for the mask's -inf: a tiny row on keys that are all 0 (2^-126 of
+        // a score is nothing either way)
+        const float fg = fmaxf(rs * info.x, 1.1754944e-38f);
         const uint64_t f2 = f2_pack(fg, fg);
         float tsum = 0.f;
         bool gave_up = C::kTurns && !warp_wait_idle(turn(half, q4), half == 0 ? (n & 1u) ^ 1u : n & 1u,

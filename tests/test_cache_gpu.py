@@ -579,3 +579,31 @@ def test_many_tiny_sequences_and_wide_groups(gla):
     for G in (1, 20, 128):
         for m in (1, 1 << 20):
             check_attention(gla, c, new, G, 1, 0, 0, False, G, max_new=m)
+
+
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+def test_tiny_queries_on_keys_that_are_all_zero(gla, max_new):
+    """Row and key scales whose product is below the fp32 range, on rows with a
+    mask: every visible key weighs the same."""
+    P, d = 32, 128
+    c = Cache(8, 1, P, d, 8, range(8))
+    c.add(0)
+    c.step(gla, [150], torch.zeros(150, 1, d).bfloat16(), bf((150, 1, d), 2))
+    out = check_attention(gla, c, [100], 2, 1, 0, 0, False, 3, max_new=max_new, qscale=2.0 ** -100)
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+def test_more_rows_than_tokens_held(gla, max_new):
+    """New rows beyond a sequence's length stand before its first token: 0."""
+    P, d = 16, 64
+    c = Cache(8, 1, P, d, 8, range(8))
+    c.add(0)
+    c.step(gla, [70], bf((70, 1, d), 1), bf((70, 1, d), 2))
+    q = bf((100, 1, d), 3).cuda()
+    out = torch.full_like(q, 7.0)
+    args = (c.k8, c.v8, c.ks, c.vs, c.tables(), ints(c.lens), ints([0, 100]), None, out)
+    gla.gla_cache_attention(q, *args, 1, 100, max_new, 1, 1, d, 8, P, 8, 1, 0, 0, d ** -0.5)
+    assert out[:30].eq(0).all() and out[30:].abs().sum() > 0
+    tail = check_attention(gla, c, [70], 1, 1, 0, 0, False, 3, max_new=max_new, pad=0)
+    assert tail.shape == (70, 1, d)
