@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kStoreThreads, (StoreCfg<D, P>::kPerSm))
       s_items[r] = static_cast<int>(sum);
       sum += n;
     }
-    if (tid == 0) s_items[p.R] = static_cast<int>(all);
+    // more runs than tokens: the rows descend or overlap, and there is no work
+    if (tid == 0) s_items[p.R] = all > p.tokens ? 0 : static_cast<int>(all);
     __syncthreads();
   }
   // an item: its first token, its rows, the head and tensor, and the slot of

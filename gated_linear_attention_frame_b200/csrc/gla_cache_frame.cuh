@@ -273,6 +273,9 @@ __global__ void __launch_bounds__(1024, 1)
       e0[r] = static_cast<int>(sum);
       sum += (cache_seq(p, r).n + TU - 1) / TU;
     }
+    // rows that descend or overlap can ask for more entries than there is room
+    // for: then there is no work
+    if (all > fs.entries_max) all = 0;
     if (tid == 0) e0[p.R] = static_cast<int>(all);
     __syncthreads();
     entries = static_cast<int>(all);

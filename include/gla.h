@@ -239,12 +239,19 @@ int gla_softmax_anchor_step(const void* q, const void* k, const void* v, const v
  *                    sequence r are rows cu_tokens[r] .. cu_tokens[r+1] - 1;
  *                    rows from cu_tokens[R] on belong to nobody and are
  *                    neither read nor written.
+ *                    cu_tokens ascends from 0 (gla_cache_plan writes it so); for
+ *                    one that does not, what the rows receive is undefined,
+ *                    but nothing outside the arrays is touched.
  *   caches           e4m3 codes [pages, Hkv, P, d]; scales fp32 [pages, Hkv],
  *                    powers of two; a value is code * scale.
  *   block_table      int32 [R, max_pages]: entry j of row r is the page of
  *                    tokens j P .. j P + P - 1.  Entries that no visible token
  *                    needs may hold anything; a key whose entry is not in 0 ..
  *                    pages - 1 is not attended.
+ * Sequences may share pages that attention reads (a common prefix under several
+ * rows of block_table), but a page that receives tokens belongs to one sequence
+ * alone: gla_cache_store does not order two writers, and gla_cache_plan returns
+ * a page once for each row that gives it up.
  * pages * P and max_pages * P must stay below 2^31 (slots are 32-bit).  Integer
  * arrays and scales are 4-byte aligned, the others 16-byte aligned.
  */

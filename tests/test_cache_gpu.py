@@ -607,3 +607,45 @@ def test_more_rows_than_tokens_held(gla, max_new):
     assert out[:30].eq(0).all() and out[30:].abs().sum() > 0
     tail = check_attention(gla, c, [70], 1, 1, 0, 0, False, 3, max_new=max_new, pad=0)
     assert tail.shape == (70, 1, d)
+
+
+@pytest.mark.parametrize("max_new", [1, 1 << 20])
+def test_row_ranges_that_descend_stay_in_bounds(gla, max_new):
+    """Offsets that go up and down give each second sequence all the rows: more
+    units than the host's bound.  The arrays' neighbours and a later call are as
+    they should be."""
+    P, d, R, N, pages = 16, 64, 64, 1100, 70
+    c = Cache(pages, 1, P, d, pages, range(pages))
+    c.add(0)
+    c.step(gla, [N], bf((N, 1, d), 1), bf((N, 1, d), 2))
+    lens, cu = ints([N] * R), ints([0, N] * (R // 2) + [0])
+    tables = c.tables().expand(R, -1).contiguous()
+    q, guard = bf((N, 1, d), 3).cuda(), torch.full((3 * N, 1, d), 5.0, dtype=torch.bfloat16).cuda()
+    gla.gla_cache_attention(q, c.k8, c.v8, c.ks, c.vs, tables, lens, cu, None, guard[N:2 * N], R, N,
+                            max_new, 1, 1, d, pages, P, pages, 1, 0, 0, d ** -0.5)
+    assert guard[:N].eq(5).all() and guard[2 * N:].eq(5).all()
+    before = [t.clone() for t in (c.k8, c.v8, c.ks, c.vs)]
+    gla.gla_cache_store(q, q, lens, cu, torch.arange(N, dtype=torch.int32, device="cuda"), *before,
+                        None, R, N, 1, d, pages, P)
+    torch.cuda.synchronize()
+    check_attention(gla, c, [N], 1, 1, 0, 0, False, 3, max_new=max_new)
+
+
+def test_a_prefix_that_two_sequences_share(gla):
+    """Two rows of the table with the same first pages."""
+    P, d = 32, 128
+    c = Cache(12, 2, P, d, 6, range(12))
+    c.add(0)
+    c.step(gla, [96], bf((96, 2, d), 1), bf((96, 2, d), 2))
+    table = c.tables().expand(2, -1).contiguous()
+    q = bf((2, 4, d), 3).cuda()
+    out = torch.empty_like(q)
+    gla.gla_cache_attention(q, c.k8, c.v8, c.ks, c.vs, table, ints([96, 96]), ints([0, 1, 2]), None,
+                            out, 2, 2, 1, 4, 2, d, 12, P, 6, 1, 0, 0, d ** -0.5)
+    one = torch.empty_like(q[:1])
+    for r in range(2):
+        gla.gla_cache_attention(q[r:r + 1].contiguous(), c.k8, c.v8, c.ks, c.vs, table[:1], ints([96]),
+                                ints([0, 1]), None, one, 1, 1, 1, 4, 2, d, 12, P, 6, 1, 0, 0,
+                                d ** -0.5)
+        # each is off by 2^-8 of itself and 2^-10 sum p |v|, |v| < 8
+        assert torch.allclose(one.float(), out[r:r + 1].float(), rtol=2 ** -7, atol=2 ** -6)
