@@ -1172,7 +1172,7 @@ int run_cache_frame(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
   const size_t pre_bytes = (static_cast<size_t>(fs.entries_max) + 1) * 8;
   fs.use_smem = e0_bytes + pre_bytes <= kScheduleSmem;
   const int64_t starts_bytes = align256(static_cast<int64_t>(fs.ctas) * 16);
-  const int64_t n_bytes = align256(static_cast<int64_t>(fs.ctas) * 4 + 16);
+  const int64_t n_bytes = align256(static_cast<int64_t>(fs.ctas) * 8);
   const int64_t desc_bytes = align256(static_cast<int64_t>(fs.ctas) * 32);
   const int64_t gpre_bytes = fs.use_smem ? 0 : align256(static_cast<int64_t>(pre_bytes));
   const int64_t part_bytes = static_cast<int64_t>(fs.ctas) * 2 * C::kPartFloats * 4;
@@ -1181,8 +1181,7 @@ int run_cache_frame(gla::CacheAttnParams p, const DeviceInfo& di, cudaStream_t s
                               stream, &ws);
   if (status != GLA_OK) return status;
   fs.starts = reinterpret_cast<int4*>(ws);
-  fs.meta = reinterpret_cast<long long*>(ws + starts_bytes);
-  fs.n = reinterpret_cast<int*>(ws + starts_bytes + 16);
+  fs.n = reinterpret_cast<int2*>(ws + starts_bytes);
   p.desc = reinterpret_cast<int*>(ws + starts_bytes + n_bytes);
   fs.prefix = reinterpret_cast<long long*>(ws + starts_bytes + n_bytes + desc_bytes);
   p.part = reinterpret_cast<float*>(ws + starts_bytes + n_bytes + desc_bytes + gpre_bytes);

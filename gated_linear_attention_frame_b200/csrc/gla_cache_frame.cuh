@@ -155,7 +155,7 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// Which of the 16 keys from `key` on a row sees: [lo, hi) and the sinks.
+// Which of the 32 keys from `key` on a row sees: [lo, hi) and the sinks.
 __device__ __forceinline__ uint32_t visible_bits(int key, int lo, int hi, int n_sink) {
   return bits_below(hi - key) & (~bits_below(lo - key) | bits_below(n_sink - key));
 }
@@ -187,8 +187,8 @@ struct SegInfo {
   int len;           // keys of the sequence
   int lo, hi, sink;  // visible keys, as in CacheSpan
   int whole, starts; // the segment is the unit; it holds the unit's first tile
-  int c0, t_unit, h, rest;  // for the join: packed row and token of the unit's start, head, tiles
-                            // after the segment
+  int c0, t_unit, h;  // for the join: packed row and token of the unit's start, head
+  int pad;
 };
 static_assert(sizeof(SegInfo) == 56, "one slot of the segment ring");
 
@@ -215,6 +215,11 @@ struct FrameCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
   static constexpr int kMinTiles = 4;  // least tiles of a CTA
+  // what a unit costs beyond its tiles (queries, first and masked tiles, result), in
+  // tiles.  Ragged prompts of up to 2048 tokens on up to 4096 keys, shares by tiles
+  // alone / with 2, 3, 4, 5, 6, 8 for a unit: d = 64 343 / 298, 287, 289, 290, 293,
+  // 302 us; d = 128 465 / -, 375, 359, 355, 347, 350 us.
+  static constexpr int kUnitTiles = D == 128 ? 6 : 3;
   // The two halves' softmax warps of one scheduler take turns (d = 128) or run
   // as they come (d = 64).  Left alone, the halves fall into step: both in the
   // softmax, then both on the tensor core.  Taking turns keeps one on each; a
@@ -236,11 +241,10 @@ constexpr int kJoinTiles = 6;  // what writing and joining partials costs, in ti
                                // d = 128: about 17 us and 2.9 us)
 
 // Where the schedule goes: starts[c] = {sequence, kv head, unit, tile} of the
-// first tile of CTA c and n[c] its number of tiles.
+// first tile of CTA c and n[c] its number of tiles (and see there).
 struct FrameSchedule {
   int4* starts;
-  int* n;
-  long long* meta;    // tiles, CTAs that share them
+  int2* n;            // tiles, CTAs that share the unit which begins here and goes on
   long long* prefix;  // used when the entries do not fit in shared memory
   int entries_max;    // host bound of the entries (units of one kv head)
   int use_smem;
@@ -249,8 +253,9 @@ struct FrameSchedule {
 };
 
 // One CTA.  Entry e = unit i of sequence r (all kv heads alike); prefix sums
-// of the tiles over the entries, then CTA c's first tile is found by two
-// searches.  Order of the tiles: sequence, kv head, unit, tile.
+// of their cost over the entries, then CTA c's first tile is found by two
+// searches.  A unit costs its tiles and kUnitTiles for its queries and its result,
+// which lie before its first tile.  Order: sequence, kv head, unit, tile.
 template <int D>
 __global__ void __launch_bounds__(1024, 1)
     gla_cache_schedule_kernel(const CacheAttnParams p, const FrameSchedule fs) {
@@ -262,6 +267,7 @@ __global__ void __launch_bounds__(1024, 1)
                        : fs.prefix;  // [entries + 1]
   const int tid = threadIdx.x;
   const int TU = 2 * fs.TQ;
+  constexpr int kUnitTiles = FrameCfg<D>::kUnitTiles;
   int entries;
   {
     const int per = (p.R + 1023) / 1024;
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(1024, 1)
         const int t = (e - e0[r]) * TU;
         const int nb = cache_span<128>(p, s, t, min(t + TU, s.n) - 1).nb;
         pre[e] = sum;
-        sum += nb;
+        sum += nb + kUnitTiles;
       }
     }
     const long long base = block_exclusive_scan<long long>(sum, scratch, total);
@@ -301,10 +307,15 @@ __global__ void __launch_bounds__(1024, 1)
     if (tid == 0) pre[entries] = total;
     __syncthreads();
   }
-  const long long tiles = total * p.Hkv;
-  // unit of tile x0 (order: sequence, kv head, unit) and the tile within it
-  auto find = [&](long long x0, int& tiles_of_unit) {
-    int lo = 0, hi = p.R;  // sequence: tiles before lo <= x0 < tiles before hi
+  const long long cost = total * p.Hkv;
+  const long long tiles = cost - static_cast<long long>(entries) * p.Hkv * kUnitTiles;
+  struct Place {
+    int4 st;            // sequence, kv head, unit, tile
+    int off, w, nt;     // cost since the unit's start, of the unit; tiles of the unit
+    long long before;   // tiles before this one
+  };
+  auto find = [&](long long x0) {  // 0 <= x0 < cost
+    int lo = 0, hi = p.R;  // sequence: cost before lo <= x0 < cost before hi
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[e0[mid]] * p.Hkv <= x0)
@@ -312,17 +323,24 @@ __global__ void __launch_bounds__(1024, 1)
       else
         hi = mid;
     }
+    const int units = e0[lo + 1] - e0[lo];
     const long long base = pre[e0[lo]];
-    const long long one = pre[e0[lo + 1]] - base;  // tiles of one kv head
+    const long long one = pre[e0[lo + 1]] - base;  // of one kv head
     const long long x = x0 - base * p.Hkv;
-    int4 st;
-    st.x = lo;
-    st.y = static_cast<int>(x / one);
+    Place f;
+    f.st.x = lo;
+    f.st.y = static_cast<int>(x / one);
     const long long in_head = x % one + base;
-    st.z = prefix_owner<long long>(pre + e0[lo], e0[lo + 1] - e0[lo], in_head);
-    st.w = static_cast<int>(in_head - pre[e0[lo] + st.z]);
-    tiles_of_unit = static_cast<int>(pre[e0[lo] + st.z + 1] - pre[e0[lo] + st.z]);
-    return st;
+    f.st.z = prefix_owner<long long>(pre + e0[lo], units, in_head);
+    const long long start = pre[e0[lo] + f.st.z];
+    f.off = static_cast<int>(in_head - start);
+    f.w = static_cast<int>(pre[e0[lo] + f.st.z + 1] - start);
+    f.nt = f.w - kUnitTiles;
+    f.st.w = max(f.off - kUnitTiles, 0);
+    const long long units_before = static_cast<long long>(e0[lo]) * p.Hkv +
+                                   static_cast<long long>(f.st.y) * units + f.st.z;
+    f.before = x0 - f.off - units_before * kUnitTiles + f.st.w;
+    return f;
   };
   // Equal shares over as many CTAs as there are tiles, cut at the nearest unit
   // (no partials, no join), where that costs no CTA more than kJoinTiles tiles;
@@ -335,36 +353,48 @@ __global__ void __launch_bounds__(1024, 1)
     const long long want = (tiles + least - 1) / least;
     ctas = static_cast<int>(want < fs.ctas ? want : fs.ctas);
     for (int c = tid; c <= ctas; c += 1024) {
-      long long x = share_lo(tiles, max(ctas, 1), c);
+      long long x = share_lo(cost, max(ctas, 1), c);
       if (c > 0 && c < ctas) {
-        int nt;
-        const int4 st = find(x, nt);
-        x += 2 * st.w >= nt ? nt - st.w : -st.w;
+        const Place f = find(x);
+        x += 2 * f.off >= f.w ? f.w - f.off : -f.off;
       }
       s_cut[c] = x;
     }
     __syncthreads();
-    const long long share = ctas > 0 ? (tiles + ctas - 1) / ctas : 0;
+    const long long share = ctas > 0 ? (cost + ctas - 1) / ctas : 0;
     int over = 0;
     for (int c = tid; c < ctas; c += 1024) over |= s_cut[c + 1] - s_cut[c] > share + kJoinTiles;
     cut = __syncthreads_or(over);
   }
-  for (int c = tid; c < fs.ctas; c += 1024) {
-    int4 st = make_int4(0, 0, 0, 0);
-    int n = 0;
-    if (c < ctas) {
-      const long long x0 = cut ? share_lo(tiles, ctas, c) : s_cut[c];
-      const long long x1 = cut ? share_lo(tiles, ctas, c + 1) : s_cut[c + 1];
-      int nt;
-      n = static_cast<int>(x1 - x0);
-      if (n > 0) st = find(x0, nt);
+  // the cuts in tiles, and the end of the unit that each cut splits
+  __shared__ long long s_end[kMaxScheduleCtas + 1];
+  for (int c = tid; c <= ctas; c += 1024) {
+    const long long x = cut && ctas > 0 ? share_lo(cost, ctas, c) : s_cut[c];
+    long long before = tiles, end = tiles;
+    if (x < cost) {
+      const Place f = find(x);
+      before = f.before;
+      end = f.st.w > 0 ? before - f.st.w + f.nt : before;
+      if (c < ctas) fs.starts[c] = f.st;
     }
-    fs.starts[c] = st;
-    fs.n[c] = n;
+    s_cut[c] = before;
+    s_end[c] = end;
   }
-  if (tid == 0) {
-    fs.meta[0] = tiles;
-    fs.meta[1] = ctas;
+  __syncthreads();
+  for (int c = tid; c < fs.ctas; c += 1024) {
+    int n = 0, last = c;
+    if (c < ctas) {
+      n = static_cast<int>(s_cut[c + 1] - s_cut[c]);
+      int hi = ctas - 1;  // first CTA from c on whose tiles reach the unit's end
+      while (last < hi) {
+        const int mid = (last + hi) >> 1;
+        if (s_cut[mid + 1] >= s_end[c + 1])
+          hi = mid;
+        else
+          last = mid + 1;
+      }
+    }
+    fs.n[c] = make_int2(n, last - c + 1);
   }
 }
 
@@ -380,7 +410,7 @@ struct FrameCursor {
 
   __device__ void init(const CacheAttnParams& p, const FrameSchedule& fs) {
     const int4 st = fs.starts[blockIdx.x];
-    left = fs.n[blockIdx.x];
+    left = fs.n[blockIdx.x].x;
     r = st.x;
     h = st.y;
     i = st.z;
@@ -507,7 +537,7 @@ __global__ void __launch_bounds__(512, 1)
   if (threadIdx.x == 0) p.desc[8 * blockIdx.x] = 0;   // nothing to join, unless set below
 
   const int used = fs.TQ * p.G;  // rows of a half in use
-  const uint32_t total = fs.n[blockIdx.x];  // tiles of this CTA
+  const uint32_t total = fs.n[blockIdx.x].x;  // tiles of this CTA
   const int gm = (65536 + p.G - 1) / p.G;
   if (warp >= 12) {
     reg_dec<C::kIssuerRegs>();
@@ -630,7 +660,6 @@ __global__ void __launch_bounds__(512, 1)
             si.c0 = cur.s.c0;
             si.t_unit = t_unit;
             si.h = cur.h;
-            si.rest = cur.v.nb - cur.t1;
           }
           // one page's share of the tile, by lane: the page of its first visible group
           const uint32_t groups =
@@ -845,18 +874,22 @@ __global__ void __launch_bounds__(512, 1)
         if (!__all_sync(0xffffffffu, base >= lo && base + C::BK <= hi && bad == 0)) {
           // hidden keys: S = -inf, written back, in a pass of its own (few tiles
           // need it, and inside the loops below its code would be fetched with
-          // theirs)
+          // theirs); 32 keys that all rows see are left alone
+          tmem_wait_ld_of(s[0]);  // the load on its way is taken again below
 #pragma unroll 1
-          for (int g = 0; g < 8; ++g) {
-            uint32_t x[16];
-            tmem_ld_16cols(ts + g * 16, x);
-            tmem_wait_ld_of(x);
-            uint32_t w = visible_bits(base + g * 16, lo, hi, p.n_sink);
-            if (bad >> g & 1u) w = 0;
+          for (int g = 0; g < 4; ++g) {
+            uint32_t w = visible_bits(base + g * 32, lo, hi, p.n_sink);
+            if (bad >> (2 * g) & 1u) w &= 0xFFFF0000u;
+            if (bad >> (2 * g) & 2u) w &= 0x0000FFFFu;
+            if (__all_sync(0xffffffffu, w == 0xFFFFFFFFu)) continue;
+            if (__any_sync(0xffffffffu, w != 0)) {
+              tmem_ld_32cols(ts + g * 32, s[0]);
+              tmem_wait_ld_of(s[0]);
+            }
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[e] = (w >> e & 1u) ? x[e] : __float_as_uint(-INFINITY);
-            tmem_st_16cols(ts + g * 16, x);
+            for (int e = 0; e < 32; ++e)
+              s[0][e] = (w >> e & 1u) ? s[0][e] : __float_as_uint(-INFINITY);
+            tmem_st_32cols(ts + g * 32, s[0]);
           }
           tmem_wait_st();
           tmem_ld_32cols(ts, s[0]);
@@ -1036,17 +1069,12 @@ __global__ void __launch_bounds__(512, 1)
             make_float2(m, l);
       if (threadIdx.x == 0 && si.starts && !whole) {
         // this unit's parts: this CTA, then every one up to the last tile
-        // (a unit is split by equal shares only)
-        const long long tiles = fs.meta[0];
-        const int ctas = static_cast<int>(fs.meta[1]);
-        const long long x_end = share_lo(tiles, ctas, blockIdx.x + 1) + si.rest;
-        const int parts = share_owner(tiles, ctas, x_end - 1) - blockIdx.x + 1;
         int* desc = p.desc + 8 * blockIdx.x;
         desc[1] = si.c0;
         desc[2] = si.t_unit;
         desc[3] = si.h;
         desc[4] = min(2 * fs.TQ, si.tokens) * p.G;
-        desc[0] = parts;
+        desc[0] = fs.n[blockIdx.x].y;
       }
       ++seg;
     }
