@@ -202,7 +202,7 @@ struct FrameCfg {
   static constexpr int kSlots = 2;                  // K tiles and V tiles held each
   static constexpr int kInfoSlots = 8;
   static constexpr int kAccO = 256;
-  static constexpr int kBarCount = 4 * kSlots + 27;
+  static constexpr int kBarCount = 4 * kSlots + 29;
   static constexpr int kOffK = 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kSlots * kTileBytes;
   static constexpr int kOffRs = kOffV + kSlots * kTileBytes;       // [2][256] row exponents
@@ -481,8 +481,9 @@ __global__ void __launch_bounds__(512, 1)
   auto kempty = [&](int s) { return bar0 + 8u * (S + s); };
   auto vfull = [&](int s) { return bar0 + 8u * (2 * S + s); };
   auto vempty = [&](int s) { return bar0 + 8u * (3 * S + s); };
-  const uint32_t qfull = bar0 + 8u * (4 * S);
-  const uint32_t qempty = bar0 + 8u * (4 * S + 1);
+  // the queries of half h are in place; every S_h of the segment is done
+  auto qfull = [&](int h) { return bar0 + 8u * (h ? 4 * S + 27 : 4 * S); };
+  auto qempty = [&](int h) { return bar0 + 8u * (h ? 4 * S + 28 : 4 * S + 1); };
   auto sfull = [&](int h) { return bar0 + 8u * (4 * S + 2 + h); };  // S_h landed
   // the first (second) 64 keys of P_h are written; P V of the first 64 is done
   auto pfull = [&](int h, int part) { return bar0 + 8u * (4 * S + (part ? 15 : 4) + h); };
@@ -509,9 +510,9 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(vfull(s), 4);
       mbar_init(vempty(s), 2);
     }
-    mbar_init(qfull, 4);
-    mbar_init(qempty, 2);
     for (int h = 0; h < 2; ++h) {
+      mbar_init(qfull(h), 4);
+      mbar_init(qempty(h), 1);
       mbar_init(sfull(h), 1);
       mbar_init(pfull(h, 0), 4);
       mbar_init(pfull(h, 1), 4);
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(512, 1)
       auto issue_s = [&](uint32_t k) {  // S of tile k of this CTA
         if (!mbar_wait_idle(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
         flags = *reinterpret_cast<volatile uint32_t*>(&s_info[k & kRing].flags);
-        if ((flags & kTileFirst) && !mbar_wait_idle(qfull, seg & 1u, abort, kCode)) return false;
+        if ((flags & kTileFirst) && !mbar_wait_idle(qfull(me), seg & 1u, abort, kCode)) return false;
         tc_fence_after();
         const uint64_t b0 = kd + (k & 1u) * kStep;
         if (lead) {
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(512, 1)
           }
           mma_commit(sfull(me));
           mma_commit(kempty(k & 1u));
-          if (flags & kTileLast) mma_commit(qempty);  // every S of the segment has been issued
+          if (flags & kTileLast) mma_commit(qempty(me));  // every S of the segment has been issued
         }
         __syncwarp();
         return true;
@@ -713,52 +714,64 @@ __global__ void __launch_bounds__(512, 1)
                                       // (bank conflicts)
     // ---- queries of segment `seg`: all rows are copied to their places as bf16
     // at once, then each thread turns its own chunks into fp16 in place, scaled
-    // per row
-    auto convert_q = [&](uint32_t seg) {
+    // per row.  The scores of the unit wait for this: four copies and kBatch rows
+    // are in work at a time (row by row it took 17 thousand cycles at d = 128).
+    auto convert_q = [&](uint32_t seg, int hf) {
       constexpr int kQChunks = D / 8, kQRows = 128 / kQChunks;
-      if (!warp_wait_idle(qempty, (seg & 1u) ^ 1u, abort, kCode)) return false;
+      constexpr int kPerHalf = 128 / kQRows, kBatch = 8;
+      static_assert(kQRows % 8 == 0 && kPerHalf % kBatch == 0, "one swizzle for all rows of a thread");
+      if (!warp_wait_idle(qempty(hf), (seg & 1u) ^ 1u, abort, kCode)) return false;
       const SegInfo& si = s_seg[seg & kRing];
       const int qc = ct % kQChunks, qr0 = ct / kQChunks;
       const __nv_bfloat16* qp = p.q + si.row0 * D + qc * 8;
       const int tokens = si.tokens;
-      auto place = [&](int row) {
-        const int lr = row & 127;
-        return qbuf(row >> 7) + (qc >> 3) * G::kAtomTileBytes + lr * 128 +
-               (((qc & 7) ^ (lr & 7)) << 4);
-      };
-#pragma unroll 1
-      for (int row = qr0; row < 256; row += kQRows) {
-        const int lr = row & 127;
+      const uint32_t place = qbuf(hf) + (qc >> 3) * G::kAtomTileBytes + qr0 * 128 +
+                             (((qc & 7) ^ (qr0 & 7)) << 4);
+#pragma unroll 4
+      for (int i = 0; i < kPerHalf; ++i) {
+        const int lr = qr0 + i * kQRows;
         const int lt = small_div(lr, gm);
-        const int t = (row >> 7) * fs.TQ + lt;
+        const int t = hf * fs.TQ + lt;
         const bool have = lr < used && t < tokens;
-        cp_async16(place(row),
-                   qp + (have ? (static_cast<int64_t>(t) * p.H + (lr - lt * p.G)) * D : 0), have);
+        const int at = have ? t * p.H + (lr - lt * p.G) : 0;  // below 2^25
+        cp_async16(place + i * (kQRows * 128), qp + static_cast<int64_t>(at) * D, have);
       }
       cp_async_commit();
       cp_async_wait<0>();
-#pragma unroll 2
-      for (int row = qr0; row < 256; row += kQRows) {
-        const uint4 x = ld_shared_v4(place(row));
-        uint32_t mx = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
-                               __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
-        mx = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll 1
+      for (int i = 0; i < kPerHalf; i += kBatch) {
+        const uint32_t at = place + i * (kQRows * 128);
+        uint4 x[kBatch];
+        uint32_t mx[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) x[e] = ld_shared_v4(at + e * (kQRows * 128));
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          mx[e] = __vmaxu2(__vmaxu2(x[e].x & 0x7FFF7FFFu, x[e].y & 0x7FFF7FFFu),
+                           __vmaxu2(x[e].z & 0x7FFF7FFFu, x[e].w & 0x7FFF7FFFu));
+        }
 #pragma unroll
         for (int o = kQChunks / 2; o > 0; o >>= 1)
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int up = row_exponent(mx);
-        const float f = exp2_int(up);
-        uint4 w;
-        w.x = pack_f16x2(bf16lo_to_f32(x.x) * f, bf16hi_to_f32(x.x) * f);
-        w.y = pack_f16x2(bf16lo_to_f32(x.y) * f, bf16hi_to_f32(x.y) * f);
-        w.z = pack_f16x2(bf16lo_to_f32(x.z) * f, bf16hi_to_f32(x.z) * f);
-        w.w = pack_f16x2(bf16lo_to_f32(x.w) * f, bf16hi_to_f32(x.w) * f);
-        st_shared_v4(place(row), w);
-        if (qc == 0) s_rs[(seg & 1u) * C::kRows + row] = static_cast<int8_t>(up);
+#pragma unroll
+          for (int e = 0; e < kBatch; ++e)
+            mx[e] = __vmaxu2(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int up = row_exponent(max(mx[e] & 0xFFFFu, mx[e] >> 16));
+          const float f = exp2_int(up);
+          uint4 w;
+          w.x = pack_f16x2(bf16lo_to_f32(x[e].x) * f, bf16hi_to_f32(x[e].x) * f);
+          w.y = pack_f16x2(bf16lo_to_f32(x[e].y) * f, bf16hi_to_f32(x[e].y) * f);
+          w.z = pack_f16x2(bf16lo_to_f32(x[e].z) * f, bf16hi_to_f32(x[e].z) * f);
+          w.w = pack_f16x2(bf16lo_to_f32(x[e].w) * f, bf16hi_to_f32(x[e].w) * f);
+          st_shared_v4(at + e * (kQRows * 128), w);
+          if (qc == 0)
+            s_rs[(seg & 1u) * C::kRows + hf * 128 + qr0 + (i + e) * kQRows] = static_cast<int8_t>(up);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(qfull);
+      if (lane == 0) mbar_arrive(qfull(hf));
       return true;
     };
     uint32_t seg = 0;
@@ -766,15 +779,21 @@ __global__ void __launch_bounds__(512, 1)
     for (uint32_t n = 0; n < total && ok; ++n) {
       const int sl = n & 1u;
       const TileInfo& info = s_info[n & kRing];
-#pragma unroll 1  // K, then V: one copy of the code
-      for (int w = 0; w < 2; ++w) {
-        if (!warp_wait_idle(rfull(w), n & 1u, abort, kCode)) {
+      // queries of half 0, K, V, queries of half 1 (whose scores come later): one
+      // copy of the code
+#pragma unroll 1
+      for (int w = 0; w < 3; ++w) {
+        if (w < 2 && !warp_wait_idle(rfull(w), n & 1u, abort, kCode)) {
           ok = false;
           break;
         }
         const uint32_t flags = *const_cast<volatile const uint32_t*>(&info.flags);
-        if (w == 0 && (flags & kTileFirst) && !convert_q(seg)) {
+        if (w != 1 && (flags & kTileFirst) && !convert_q(seg, w >> 1)) {
           ok = false;
+          break;
+        }
+        if (w == 2) {
+          if (flags & kTileLast) ++seg;
           break;
         }
         uint4 x[kPasses];
@@ -829,7 +848,6 @@ __global__ void __launch_bounds__(512, 1)
           mbar_arrive(w ? vfull(sl) : kfull(sl));
           mbar_arrive(rempty(w));  // every code has been used: no load of one is outstanding
         }
-        if (w == 1 && (flags & kTileLast)) ++seg;
       }
     }
   } else {
