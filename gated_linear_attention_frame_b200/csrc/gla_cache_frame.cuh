@@ -6,10 +6,10 @@
 // query, visible key and head.  One work unit = 256 query rows (tokens x the
 // heads that share a key/value head) of one sequence and key/value head, held
 // as two halves of 128 rows; its visible keys are cut into tiles of 128.  The
-// tiles of all units are laid end to end and dealt out evenly to one CTA per
-// SM (gla_cache_schedule_kernel finds where each CTA begins); a unit that ends
-// up in several CTAs leaves a partial (O, m, l) in each, joined by
-// gla_cache_join_kernel.
+// tiles of all units, and a fixed cost before each unit, are laid end to end and
+// dealt out evenly to one CTA per SM (gla_cache_schedule_kernel finds where each
+// CTA begins); a unit that ends up in several CTAs leaves a partial (O, m, l) in
+// each, joined by gla_cache_join_kernel.
 //
 // Both halves of a unit share each key/value tile, because every tile has to
 // be converted first: tcgen05 wants both operands of a product in one type,
@@ -24,6 +24,8 @@
 //   S_h = Q_h K^T   A = Q half [128 x d] K-major, B = K tile [128 keys] K-major
 //   O_h += P_h V    A = P_h in TMEM (fp16, over the columns of S_h),
 //                   B = V tile [128 keys x d] MN-major
+// Each half's queries have their own buffer and barriers: half 0 takes the next
+// unit's while half 1 still works on the old one.
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d columns each).  One issuing
 // warp per half: P V of tile j (in two steps of 64 keys, as P is written), then
 // S of tile j + 1 into the same columns (the tensor core runs one thread's
@@ -38,9 +40,9 @@
 // Warp roles: 0-3 / 4-7 softmax and epilogue of half 0 / 1, 8-11 converters,
 // 12 / 13 MMA issuers of half 0 / 1, 14 producer (15 idle: it completes the
 // register group).
-// Measured (d = 128): 3680 queries x 14976 visible keys x 24 heads in 801 us,
-// 0.85 PFLOP/s, 0.60 of the sustained bf16 rate.  A tile takes about 5000 cycles
-// of 2048 on the tensor core; the rest is the chain scores -> exponentials ->
+// Measured (d = 128): 3680 queries x 14976 visible keys x 24 heads in 791 us,
+// 0.86 PFLOP/s, 0.61 of the sustained bf16 rate.  A tile takes about 4700 cycles
+// of 2048 on the tensor core, a unit 3 (d = 64) to 6 tiles more; the rest is the chain scores -> exponentials ->
 // P V -> next scores of two halves, one warp a scheduler each.  The roles share
 // the instruction cache: code size is time here (156 KB of code ran 1.3 times as
 // long as 97 KB), hence the rolled loops and cold passes.
@@ -225,9 +227,10 @@ struct FrameCfg {
   // softmax, then both on the tensor core.  Taking turns keeps one on each; a
   // lone warp is then bound by its instructions, not by the exponential unit,
   // so all exponentials go there.  Measured, turns / as they come with one pair
-  // of exponentials in four on the FMA pipe: 801 / about 880 us (d = 128, 3680
-  // queries, 14720 keys, 24 heads), 365 / 348 us (d = 64 ragged prompts: half
-  // the tensor work, little to hide behind).
+  // of exponentials in four on the FMA pipe (before units had their cost in the
+  // schedule): 801 / about 880 us (d = 128, 3680 queries, 14720 keys, 24 heads),
+  // 365 / 348 us (d = 64 ragged prompts: half the tensor work, little to hide
+  // behind).
   static constexpr bool kTurns = D == 128;
   // registers a thread: 128 at launch (512 threads); 256 softmax threads, 128
   // converters, 128 issuers and producer
