@@ -9,6 +9,7 @@ compared bit for bit.  The attention's bound is derived, per element:
   weights below 2^-33 of the largest vanish: 2^-33 * keys * max|v| < 2^-20 max|v|
 """
 
+import math
 import random
 
 import numpy as np
@@ -649,3 +650,42 @@ def test_a_prefix_that_two_sequences_share(gla):
                                 d ** -0.5)
         # each is off by 2^-8 of itself and 2^-10 sum p |v|, |v| < 8
         assert torch.allclose(one.float(), out[r:r + 1].float(), rtol=2 ** -7, atol=2 ** -6)
+
+
+def test_more_units_than_shared_memory_holds(gla):
+    """22 thousand units of two tokens: the schedule's sums lie in the workspace.
+    Both kernels against each other, and the first rows against the oracle."""
+    P, d, G, R, T, W = 64, 64, 128, 4, 11000, 64
+    pages = R * -(-T // P)
+    c = gla.rollout_cache(R, pages, 1, d, pages // R, page_tokens=P, window_frames=W)
+    k, v, q = (bf((R * T, h, d), 60 + h + e).cuda() for e, h in enumerate((1, 1, G)))
+    plan = gla.cache_plan(c, ints([T] * R), R * T)
+    gla.cache_store(c, plan, k, v)
+    a = gla.cache_attention(c, plan, q, max_new=T)
+    b = gla.cache_attention(c, plan, q, max_new=0)
+    assert plan.status.item() == 0
+    # each is off by 2^-8 of itself and 2^-10 sum p |v|, |v| < 8
+    for i in range(0, R * T, 4000):
+        assert torch.allclose(a[i:i + 4000].float(), b[i:i + 4000].float(), rtol=2 ** -7,
+                              atol=2 ** -6)
+    n = 128  # two pages; the window leaves the first token behind at 64
+    x, y = (oracle_values(t[:n, 0], P) for t in (k, v))
+    s = q[:n].double().cpu().numpy() @ x.T * d ** -0.5
+    at = np.arange(n)
+    seen = (at[None, :] <= at[:, None]) & (at[None, :] > at[:, None] - W)
+    s = np.where(seen[:, None, :], s, -np.inf)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    ref, mag = ((p @ t) / p.sum(-1, keepdims=True) for t in (y, np.abs(y)))
+    err = np.abs(a[:n].double().cpu().numpy() - ref)
+    assert np.all(err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * mag + 2.0 ** -20 * np.abs(y).max())
+
+
+def oracle_values(x, P):
+    """What the cache holds of one head's rows, written page by page: e4m3 with
+    the smallest power of two that takes each page's largest value."""
+    x = x.double().cpu()
+    out = torch.empty_like(x)
+    for i in range(0, x.shape[0], P):
+        step = 2.0 ** math.ceil(math.log2(x[i:i + P].abs().max().item() / 448))
+        out[i:i + P] = (x[i:i + P] / step).float().to(torch.float8_e4m3fn).double() * step
+    return out.numpy()
