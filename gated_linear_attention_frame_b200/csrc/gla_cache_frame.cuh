@@ -152,6 +152,16 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// exp2_poly3_x2 for arguments without an upper end: the weights of 64 keys are
+// computed before their maximum is known, and from 129 on the exponent field would
+// run into the sign.  From kExp2Top on the result is 2^kExp2Top, beyond every sum
+// that passes for right.
+constexpr float kExp2Top = 127.0f;
+
+__device__ __forceinline__ void exp2_poly3_any_x2(float a0, float a1, float& x0, float& x1) {
+  exp2_poly3_x2(fminf(a0, kExp2Top), fminf(a1, kExp2Top), x0, x1);
+}
+
 // Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
@@ -1000,7 +1010,7 @@ __global__ void __launch_bounds__(512, 1)
                                  f2, s2),
                           a0, a1);
                 if (!C::kTurns && (e & 3) == 0) {
-                  exp2_poly3_x2(a0, a1, y0, y1);
+                  exp2_poly3_any_x2(a0, a1, y0, y1);
                 } else {
                   y0 = ex2_approx(a0);
                   y1 = ex2_approx(a1);
