@@ -50,7 +50,7 @@
 
 #include "gla_cache_token.cuh"
 #include "gla_increment.cuh"  // warp_wait
-#include "gla_softmax_anchor.cuh"  // exp2_poly3_x2
+#include "gla_softmax_anchor.cuh"  // exp2_poly3_parts_x2
 
 namespace gla {
 
@@ -152,14 +152,34 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-// exp2_poly3_x2 for arguments without an upper end: the weights of 64 keys are
-// computed before their maximum is known, and from 129 on the exponent field would
-// run into the sign.  From kExp2Top on the result is 2^kExp2Top, beyond every sum
-// that passes for right.
+// exp2_poly3_x2 for any argument.  The weights of 64 keys are computed before
+// their maximum is known, and from 129 on the exponent field would run into the
+// sign: from kExp2Top on the result is 2^kExp2Top, beyond every sum that passes for
+// right.  A NaN stays one (a row that is not finite must not come out as 0): the
+// bounds hand it on, and 2^n is multiplied in, where an integer added to the
+// exponent field would make a number of it.
 constexpr float kExp2Top = 127.0f;
 
+__device__ __forceinline__ float clamp_nan(float x, float lo, float hi) {
+  float y;
+  asm("{\n\t.reg .f32 t;\n\t"
+      "min.NaN.f32 t, %1, %3;\n\t"
+      "max.NaN.f32 %0, t, %2;\n\t}\n"
+      : "=f"(y)
+      : "f"(x), "f"(lo), "f"(hi));
+  return y;
+}
+
 __device__ __forceinline__ void exp2_poly3_any_x2(float a0, float a1, float& x0, float& x1) {
-  exp2_poly3_x2(fminf(a0, kExp2Top), fminf(a1, kExp2Top), x0, x1);
+  float t0, t1;
+  uint64_t t;
+  const uint64_t p = exp2_poly3_parts_x2(
+      f2_pack(clamp_nan(a0, -126.0f, kExp2Top), clamp_nan(a1, -126.0f, kExp2Top)), t);
+  f2_unpack(t, t0, t1);
+  // bits of t << 23: n in the exponent field; with the field of 1.0: 2^n
+  const uint64_t e = f2_pack(__int_as_float((__float_as_int(t0) << 23) + 0x3F800000),
+                             __int_as_float((__float_as_int(t1) << 23) + 0x3F800000));
+  f2_unpack(f2_mul(p, e), x0, x1);
 }
 
 // Bits 0 .. n - 1 (none for n <= 0, all for n >= 32).

@@ -141,14 +141,19 @@ __device__ __forceinline__ float exp2_poly3(float x) {
   return __int_as_float(__float_as_int(p) + (__float_as_int(t) << 23));
 }
 
-// The same for two lanes with the packed pair arithmetic.
-__device__ __forceinline__ void exp2_poly3_x2(float a0, float a1, float& x0, float& x1) {
-  const uint64_t x = f2_pack(fmaxf(a0, -126.0f), fmaxf(a1, -126.0f));
-  const uint64_t t = f2_add(x, f2_pack(12582912.0f, 12582912.0f));
+// Two lanes with the packed pair arithmetic: 2^r, and t, whose low bits are n.
+__device__ __forceinline__ uint64_t exp2_poly3_parts_x2(uint64_t x, uint64_t& t) {
+  t = f2_add(x, f2_pack(12582912.0f, 12582912.0f));
   const uint64_t r = f2_sub(x, f2_sub(t, f2_pack(12582912.0f, 12582912.0f)));
   uint64_t p = f2_fma(f2_pack(kExp2C3, kExp2C3), r, f2_pack(kExp2C2, kExp2C2));
   p = f2_fma(p, r, f2_pack(kExp2C1, kExp2C1));
-  p = f2_fma(p, r, f2_pack(kExp2C0, kExp2C0));
+  return f2_fma(p, r, f2_pack(kExp2C0, kExp2C0));
+}
+
+// exp2_poly3 for two lanes.
+__device__ __forceinline__ void exp2_poly3_x2(float a0, float a1, float& x0, float& x1) {
+  uint64_t t;
+  const uint64_t p = exp2_poly3_parts_x2(f2_pack(fmaxf(a0, -126.0f), fmaxf(a1, -126.0f)), t);
   float p0, p1, t0, t1;
   f2_unpack(p, p0, p1);
   f2_unpack(t, t0, t1);
