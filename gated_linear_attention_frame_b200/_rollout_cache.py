@@ -5,6 +5,8 @@ its tensors.
 As in _binding, only argument marshalling happens here.  Beside the library's
 own checks the wrappers compare dtypes and element counts with the sizes that
 are passed, and run on the device of the tensors, whichever device is current.
+Tensors that a call with `stream` allocates belong to that stream, as those made
+under torch.cuda.stream() do.
 
     cache = gla.rollout_cache(sequences=8, pages=4096, kv_heads=24, d=128,
                               max_pages=512, page_tokens=64, frame_tokens=3680,
@@ -16,6 +18,7 @@ are passed, and run on the device of the tensors, whichever device is current.
 
 from __future__ import annotations
 
+import contextlib
 import math
 from dataclasses import dataclass
 
@@ -128,6 +131,16 @@ def gla_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lens
           window_frames, n_sink, scale), stream)
 
 
+def _allocating_for(stream, device):
+    """The context to allocate a call's tensors in: memory that the current stream
+    gave back may still be in use there, so a call on another stream takes its own."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_b._stream(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 @dataclass
 class RolloutCache:
     """The tensors of a paged rollout cache and its mask.  k, v and their
@@ -193,9 +206,10 @@ def cache_plan(cache: RolloutCache, new_lens, tokens: int, stream=None) -> Cache
     more).  Updates the cache's lengths, tables and free pages."""
     R, max_pages = cache.block_table.shape
     dev = cache.lens.device
-    plan = CachePlan(torch.empty(R + 1, dtype=_I32, device=dev),
-                     torch.empty(tokens, dtype=_I32, device=dev),
-                     torch.empty(1, dtype=_I32, device=dev))
+    with _allocating_for(stream, dev):
+        plan = CachePlan(torch.empty(R + 1, dtype=_I32, device=dev),
+                         torch.empty(tokens, dtype=_I32, device=dev),
+                         torch.empty(1, dtype=_I32, device=dev))
     gla_cache_plan(cache.lens, cache.held, new_lens, cache.free_count, cache.free_pages,
                    cache.block_table, cache.lens, cache.held, cache.free_count, plan.cu_tokens,
                    plan.slots, plan.status, R, max_pages, cache.k.shape[0], cache.page_tokens,
@@ -228,7 +242,8 @@ def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=
     if gate_z is not None and gate_z.shape != q.shape:
         raise ValueError("gate_z must have q's shape, got %s" % (tuple(gate_z.shape),))
     if out is None:
-        out = torch.empty_like(q)
+        with _allocating_for(stream, q.device):
+            out = torch.empty_like(q)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape, got %s" % (tuple(out.shape),))
     if max_new is None:
