@@ -231,7 +231,9 @@ def cache_store(cache: RolloutCache, plan: CachePlan, k, v, nonfinite=None, stre
 def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=None, out=None,
                     max_new=None, stream=None):
     """Attention of the step's queries q [tokens, H, d] over the cache (which
-    already holds the step's keys and values); returns out.  `max_new`: about
+    already holds the step's keys and values); returns out.  Rows that belong to no
+    sequence (behind the last one, or all of them when the plan refused the step:
+    plan.status) are 0, or as they were in the caller's `out`.  `max_new`: about
     the most new tokens of one sequence, as far as the host knows; it picks the
     kernel, never what is computed (default: the mean, tokens / sequences)."""
     pages, Hkv, P, d = cache.k.shape
@@ -243,7 +245,7 @@ def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=
         raise ValueError("gate_z must have q's shape, got %s" % (tuple(gate_z.shape),))
     if out is None:
         with _allocating_for(stream, q.device):
-            out = torch.empty_like(q)
+            out = torch.zeros_like(q)  # the kernels leave rows of no sequence alone
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape, got %s" % (tuple(out.shape),))
     if max_new is None:
