@@ -488,8 +488,9 @@ def gla_set_wait_limit_ns(ns: int) -> None:
 
 
 def gla_inject_stall(tile: int) -> None:
-    """Testing hook: the next state-increment launch withholds one tile on its
-    first CTA, so that a wait runs out (see include/gla.h)."""
+    """Testing hook: the next launch of the state-increment kernel or of the cached
+    attention of many queries withholds one tile on its first CTA, so that a wait
+    runs out (see include/gla.h)."""
     st = load_library().gla_inject_stall(int(tile))
     if st != GLA_OK:
         raise GLAError(st, "gla_inject_stall")

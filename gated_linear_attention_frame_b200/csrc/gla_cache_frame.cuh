@@ -579,7 +579,9 @@ __global__ void __launch_bounds__(512, 1)
     if (me < 2) {
       // ---------------------------------------------------------- MMA issuers
       // The whole warp walks the tiles, so that addresses and descriptors stay
-      // in uniform registers; one lane issues and commits.
+      // in uniform registers; one lane issues and commits.  A wait that runs out
+      // ends the loop for all lanes at once (warp_wait_idle): lanes that went
+      // apart would meet at different barriers.
       constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
       constexpr uint64_t kStep = C::kTileBytes >> 4;  // next buffer, in the address field
@@ -590,9 +592,9 @@ __global__ void __launch_bounds__(512, 1)
       const bool lead = elect_one();
       uint32_t seg = 0, flags = 0;
       auto issue_s = [&](uint32_t k) {  // S of tile k of this CTA
-        if (!mbar_wait_idle(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
+        if (!warp_wait_idle(kfull(k & 1u), (k >> 1) & 1u, abort, kCode)) return false;
         flags = *reinterpret_cast<volatile uint32_t*>(&s_info[k & kRing].flags);
-        if ((flags & kTileFirst) && !mbar_wait_idle(qfull(me), seg & 1u, abort, kCode)) return false;
+        if ((flags & kTileFirst) && !warp_wait_idle(qfull(me), seg & 1u, abort, kCode)) return false;
         tc_fence_after();
         const uint64_t b0 = kd + (k & 1u) * kStep;
         if (lead) {
@@ -611,9 +613,9 @@ __global__ void __launch_bounds__(512, 1)
       bool ok = total > 0 && issue_s(0);
       for (uint32_t n = 0; n < total && ok; ++n) {
         const uint32_t now = flags;  // of tile n
-        if (((now & kTileFirst) && !mbar_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
-            !mbar_wait_idle(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
-            !mbar_wait_idle(pfull(me, 0), n & 1u, abort, kCode))
+        if (((now & kTileFirst) && !warp_wait_idle(ofree(me), (seg & 1u) ^ 1u, abort, kCode)) ||
+            !warp_wait_idle(vfull(n & 1u), (n >> 1) & 1u, abort, kCode) ||
+            !warp_wait_idle(pfull(me, 0), n & 1u, abort, kCode))
           break;
         tc_fence_after();
         const uint64_t b0 = vd + (n & 1u) * kStep;
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(512, 1)
           mma_commit(pvdone(me));
         }
         __syncwarp();
-        if (!mbar_wait_idle(pfull(me, 1), n & 1u, abort, kCode)) break;
+        if (!warp_wait_idle(pfull(me, 1), n & 1u, abort, kCode)) break;
         tc_fence_after();
         if (lead) {
 #pragma unroll
@@ -648,6 +650,13 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t chunk = static_cast<uint32_t>(D) << p.p_shift;  // one page of one head
       const int copies = 128 >> p.p_shift, per = P >> 4;  // pages of a tile, groups of a page
       uint32_t n = 0, seg = 0, issued = 0;  // copies of K and V tiles begun
+      // gla_inject_stall (testing): CTA 0 withholds one tile, once
+      long long stall = -1;
+      if (blockIdx.x == 0) {
+        stall = *const_cast<volatile long long*>(&g_gla_stall_tile);
+        __syncwarp();
+        if (lane == 0 && stall >= 0) g_gla_stall_tile = -1;
+      }
       bool ok = true;
       FrameCursor cur;
       for (cur.init(p, fs); cur.live && ok; cur.next(p, fs), ++seg) {
@@ -723,6 +732,7 @@ __global__ void __launch_bounds__(512, 1)
               ok = false;
               break;
             }
+            if (n == stall) continue;  // nothing arrives on rfull for this tile
             if (lane == 0) mbar_arrive_expect_tx(rfull(w), bytes);
             __syncwarp();
             ++issued;
@@ -1129,6 +1139,8 @@ __global__ void __launch_bounds__(512, 1)
       }
       ++seg;
     }
+    __syncwarp();
+    tmem_wait_ld();  // a load on its way when a wait ran out
   }
 
   __syncwarp();

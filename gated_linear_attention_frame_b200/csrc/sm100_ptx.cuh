@@ -85,8 +85,9 @@ constexpr uint64_t kWaitLimitDefaultNs = 1000000000ull;
 __device__ uint64_t g_gla_wait_limit_ns = kWaitLimitDefaultNs;
 
 // Test hook set by gla_inject_stall(): the next launch of the state-increment
-// kernel withholds, on CTA 0, the loads of this tile of its sequence and
-// their barrier arrival, so that the wait for that tile runs out.  -1: none.
+// kernel or of the cached attention of many queries withholds, on CTA 0, the
+// loads of this tile of its sequence and their barrier arrival, so that the
+// wait for that tile runs out.  -1: none.
 // The kernel clears it when it takes it.
 __device__ long long g_gla_stall_tile = -1;
 

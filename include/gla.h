@@ -579,11 +579,12 @@ int gla_set_workspace_retention(unsigned long long bytes);
  *   wait on the current device (default one second; ns = 0 restores it).
  *   Returns GLA_OK or GLA_ERR_LAUNCH.
  *
- * gla_inject_stall -- the next launch of the state-increment kernel on the
+ * gla_inject_stall -- the next launch of the state-increment kernel or of the
+ *   cached attention of many queries (whichever comes first) on the
  *   current device withholds, on its first CTA, the loads of the tile with
  *   index `tile` in that CTA's sequence (0 = its first tile), once.  The wait
- *   for that tile runs out after the wait limit; the kernel then sets bit 0
- *   of the fault word (gla_device_fault), lets its copies in flight land,
+ *   for that tile runs out after the wait limit; the kernel then sets its bit (0
+ *   or 8) of the fault word (gla_device_fault), lets its copies in flight land,
  *   frees its tensor memory and returns, and that call's outputs are invalid.
  *   The next call runs normally.  tile < 0 disarms it.
  *   Returns GLA_OK or GLA_ERR_LAUNCH.
