@@ -1226,7 +1226,9 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   if (max_new < 0 || p.H < 0 || p.Hkv < 0 || p.H > (1 << 16)) return GLA_ERR_SHAPE;
   if (p.max_pages < 0 || static_cast<int64_t>(p.max_pages) * P > INT32_MAX - 256)
     return GLA_ERR_SHAPE;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return GLA_ERR_SHAPE;  // rejects NaN and inf
+  // rejects NaN and infinity, and what becomes infinite in the kernels' base 2
+  p.sl2 = static_cast<float>(1.4426950408889634 * scale);
+  if (!(scale > 0.0f) || !std::isfinite(p.sl2)) return GLA_ERR_SHAPE;
   if (p.R == 0 || p.tokens == 0 || p.H == 0) return GLA_OK;
   if (p.Hkv == 0 || p.H % p.Hkv != 0 || p.H / p.Hkv > 128) return GLA_ERR_SHAPE;
   if (p.q == nullptr || p.out == nullptr || p.lens == nullptr || p.cu == nullptr)
@@ -1244,7 +1246,6 @@ int cache_attention_impl(gla::CacheAttnParams p, int max_new, int d, int P, floa
   p.G = p.H / p.Hkv;
   p.p_shift = page_shift(P);
   p.by_f = gla::FastDiv::make(static_cast<uint32_t>(p.F));
-  p.sl2 = static_cast<float>(1.4426950408889634 * scale);
   if (p.pages == 0 || p.max_pages == 0) p.max_pages = p.pages = 0;  // no key is visible
   DeviceInfo di;
   if ((st = device_setup(&di)) != GLA_OK) return st;

@@ -330,11 +330,13 @@ int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu
  * a sequence's end may hold anything.
  *   max_new  the largest number of new tokens of one sequence, as far as the
  *            host knows it: it picks the kernel, not the result's range.
- *   scale    score scale, > 0 and finite (1 / sqrt(d) for the anchor layer).
+ *   scale    score scale, > 0, scale log2(e) finite in fp32 (1 / sqrt(d) for the
+ *            anchor layer).
  * Precision: e4m3 codes enter the products exactly, q scaled by a power of two
  * per row (exact), the softmax weights rounded to fp16; scores, sums and
- * outputs accumulate in fp32, out is rounded once to bf16.  The same inputs
- * give the same bits.  In calls of more than 64 query rows a sequence and
+ * outputs accumulate in fp32, out is rounded once to bf16.  Scores of 2^23 and more
+ * (where one fp32 step is a whole factor of two between weights) are out of range.
+ * The same inputs give the same bits.  In calls of more than 64 query rows a sequence and
  * key/value head, 128 neighbouring keys share one scale inside the kernel: a
  * page whose scale is within 2^15 of the largest among them enters exactly, one
  * 2^25 or more below it counts as zeros.
