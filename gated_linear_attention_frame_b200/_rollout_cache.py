@@ -13,7 +13,11 @@ under torch.cuda.stream() do.
                               window_frames=4, n_sink=256)
     plan = gla.cache_plan(cache, new_lens, tokens)      # once a step
     gla.cache_store(cache, plan, k, v)                  # each layer (its own pools)
-    out = gla.cache_attention(cache, plan, q)
+    out = gla.cache_attention(cache, plan, q, max_new=3680)
+
+max_pages bounds the tokens of a whole rollout, not of its window: a block table has
+an entry for every page a sequence has had (here 512 * 64 tokens, eight frames).  A
+step that does not fit is refused as a whole: plan.status, on the GPU.
 """
 
 from __future__ import annotations
@@ -233,9 +237,13 @@ def cache_attention(cache: RolloutCache, plan: CachePlan, q, gate_z=None, scale=
     """Attention of the step's queries q [tokens, H, d] over the cache (which
     already holds the step's keys and values); returns out.  Rows that belong to no
     sequence (behind the last one, or all of them when the plan refused the step:
-    plan.status) are 0, or as they were in the caller's `out`.  `max_new`: about
-    the most new tokens of one sequence, as far as the host knows; it picks the
-    kernel, never what is computed (default: the mean, tokens / sequences)."""
+    plan.status) are 0, or as they were in the caller's `out`.  `max_new`:
+    the most new tokens of one sequence, as far as the host knows.  It picks the
+    kernel of the whole call; both give the definition's result (include/gla.h
+    has their precision), the wrong one slowly.  The default, the mean tokens /
+    sequences, suits steps in which all sequences get about the same; a ragged
+    step (a prompt among single tokens) or one with many rows of no sequence
+    should pass it."""
     pages, Hkv, P, d = cache.k.shape
     R, max_pages = cache.block_table.shape
     N, H = q.shape[0], q.shape[1]

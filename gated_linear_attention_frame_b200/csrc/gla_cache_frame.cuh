@@ -40,8 +40,9 @@
 // Warp roles: 0-3 / 4-7 softmax and epilogue of half 0 / 1, 8-11 converters,
 // 12 / 13 MMA issuers of half 0 / 1, 14 producer (15 idle: it completes the
 // register group).
-// Measured (d = 128): 3680 queries x 14976 visible keys x 24 heads in 791 us,
-// 0.86 PFLOP/s, 0.61 of the sustained bf16 rate.  A tile takes about 4700 cycles
+// Measured (d = 128): 3680 queries x 14976 visible keys x 24 heads in 792-809 us,
+// 0.84-0.86 PFLOP/s, 0.60 of the sustained bf16 rate (0.50 of the burst rate, which
+// the clock of so short a run is nearer to).  A tile takes about 4700 cycles
 // of 2048 on the tensor core, a unit 3 (d = 64) to 6 tiles more; the rest is the chain scores -> exponentials ->
 // P V -> next scores of two halves, one warp a scheduler each.  The roles share
 // the instruction cache: code size is time here (156 KB of code ran 1.3 times as
@@ -49,7 +50,7 @@
 #pragma once
 
 #include "gla_cache_token.cuh"
-#include "gla_increment.cuh"  // warp_wait
+#include "gla_common.cuh"
 #include "gla_softmax_anchor.cuh"  // exp2_poly3_parts_x2
 
 namespace gla {
@@ -260,7 +261,7 @@ struct FrameCfg {
   // of exponentials in four on the FMA pipe (before units had their cost in the
   // schedule): 801 / about 880 us (d = 128, 3680 queries, 14720 keys, 24 heads),
   // 365 / 348 us (d = 64 ragged prompts: half the tensor work, little to hide
-  // behind).
+  // behind; the bounds on the polynomial's argument add 2%).
   static constexpr bool kTurns = D == 128;
   // registers a thread: 128 at launch (512 threads); 256 softmax threads, 128
   // converters, 128 issuers and producer

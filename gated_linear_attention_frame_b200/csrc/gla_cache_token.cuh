@@ -8,8 +8,9 @@
 // vs the scales of the key's page.  A row that sees no key gives 0.
 //
 // With few query rows a call is bound by reading the codes once from HBM: 2 d
-// bytes a key and head.  One work unit = 16 query rows (tokens x the heads
-// that share a key/value head, padded) of one sequence and key/value head; its
+// bytes a key and head.  One work unit = 8 or 16 query rows (tokens x the heads
+// that share a key/value head, padded; 8 where all rows of a sequence fit) of one
+// sequence and key/value head; its
 // visible keys are cut into blocks of 32.  All blocks of all units are laid
 // end to end and dealt out evenly to the CTAs, so a long sequence is split as
 // finely as the GPU is wide whatever the mix of lengths; a unit that ends up
@@ -30,9 +31,9 @@
 // folded into the exponent, P' = 2^(x + log2 vs - m + kBias), and taken out
 // of the row sum again block by block.
 // Measured (d = 128): 64 sequences x 8 key/value heads x 8 queries, 1.96 GB of
-// codes, 361 us (5.4 TB/s); 2 sequences of 200 thousand keys x 24 heads, 2.28 GB,
-// 416 us (5.5 TB/s).  Small calls are bound by the start: sums over the lengths,
-// table, codes, one after the other.
+// codes, 367-393 us (5.0-5.3 TB/s); 2 sequences of 200 thousand keys x 24 heads,
+// 2.28 GB, 393-425 us (5.4-5.8 TB/s); ranges over several GPUs.  Small calls are
+// bound by the start: sums over the lengths, table, codes, one after the other.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,7 +43,8 @@
 
 namespace gla {
 
-// Division of 0 <= n < 2^31 by d >= 1 as a multiplication and a shift (m = 2^32
+// Division of 0 <= n < 2^31 by d >= 1 as a multiplication and a shift (division by
+// invariant integers, Granlund and Montgomery 1994: m = 2^32
 // (2^s - d) / d + 1, s = ceil(log2 d); exact for every 32-bit n): the kernels
 // divide by the frame and the tile in many places, and a division is 25
 // instructions.
@@ -75,11 +77,12 @@ struct CacheAttnParams {
   int pages, max_pages, p_shift;  // P = 1 << p_shift
   int F, W, n_sink;
   float sl2;  // scale * log2(e)
-  // token kernel: a tile of 16 rows holds `tile_t` tokens (all G heads of each),
-  // or, where G > 16, one of `tile_c` parts of one token's heads
+  // token kernel: a tile of R = 8 or 16 rows holds `tile_t` tokens (all G heads of
+  // each), or, where G > R, one of `tile_c` parts of one token's heads
   int tile_t, tile_c;
   FastDiv by_f, by_tile;  // by F; by tile_t, or tile_c where that is not 1
-  // split units: per CTA two partials of kPartRows rows (fp32 O, then m, l)
+  // split units: per CTA two partials of a unit's rows (fp32 O, then m, l: TokenCfg's
+  // and FrameCfg's kPartFloats)
   // and one descriptor
   float* part;
   int* desc;

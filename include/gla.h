@@ -252,6 +252,8 @@ int gla_softmax_anchor_step(const void* q, const void* k, const void* v, const v
  * rows of block_table), but a page that receives tokens belongs to one sequence
  * alone: gla_cache_store does not order two writers, and gla_cache_plan returns
  * a page once for each row that gives it up.
+ * max_pages bounds all tokens that a sequence has had, those behind its window
+ * included: their entries stay in the table's row when their pages go back.
  * pages * P and max_pages * P must stay below 2^31 (slots are 32-bit).  Integer
  * arrays and scales are 4-byte aligned, the others 16-byte aligned.
  */
@@ -329,17 +331,23 @@ int gla_cache_store(const void* k, const void* v, const int* lens, const int* cu
  * gla_cache_store never writes) must not stand in a visible slot; slots behind
  * a sequence's end may hold anything.
  *   max_new  the largest number of new tokens of one sequence, as far as the
- *            host knows it: it picks the kernel, not the result's range.
+ *            host knows it: max_new * H / Hkv picks the kernel of the whole call (up
+ *            to 64: single tokens and short runs; above: frames and prompts).
+ *            Either computes any call within the precision below; they round
+ *            differently, and only the second shares a scale among 128 keys.  The
+ *            wrong one is slow: with too small a value the keys are read again for
+ *            every 8 or 16 query rows, with too large a one a single token costs a
+ *            unit of 256 rows.
  *   scale    score scale, > 0, scale log2(e) finite in fp32 (1 / sqrt(d) for the
  *            anchor layer).
  * Precision: e4m3 codes enter the products exactly, q scaled by a power of two
- * per row (exact), the softmax weights rounded to fp16; scores, sums and
- * outputs accumulate in fp32, out is rounded once to bf16.  Scores of 2^23 and more
- * (where one fp32 step is a whole factor of two between weights) are out of range.
- * The same inputs give the same bits.  In calls of more than 64 query rows a sequence and
- * key/value head, 128 neighbouring keys share one scale inside the kernel: a
- * page whose scale is within 2^15 of the largest among them enters exactly, one
- * 2^25 or more below it counts as zeros.
+ * per row (exact), the softmax weights rounded to fp16 (some of them within 2^-13
+ * before that); scores, sums and outputs accumulate in fp32, out is rounded once to
+ * bf16.  Scores of 2^23 and more (where one fp32 step is a whole factor of two
+ * between weights) are out of range.  The same inputs give the same bits.  In the
+ * kernel of frames and prompts 128 neighbouring keys share one scale: a page whose
+ * scale is within 2^15 of the largest among them enters exactly, one 2^25 or more
+ * below it counts as zeros, one between is rounded.
  * Memory: a workspace from the library's pool, freed on `stream`.
  */
 int gla_cache_attention(const void* q, const void* k_cache, const void* v_cache,
